@@ -8,6 +8,7 @@ host batches).
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Sequence
 
 import torch
@@ -19,7 +20,8 @@ from ._lib import (VSA_BF16, VSA_CUBE, VSA_F32, VSA_SELECT_CUBE, VSA_SELECT_GIVE
                    vsa_build_mask, vsa_get_device_error, vsa_layout_rows, vsa_mask_workspace_size, vsa_max_kv, vsa_num_blocks,
                    vsa_pattern_window, vsa_permute, vsa_profile_heads, vsa_profile_rows, vsa_profile_workspace_size,
                    vsa_sparse_attn_fwd, vsa_sparse_attn_fwd_natural, vsa_unpermute, SemParams, make_sem_params,
-                   vsa_quantize_fp8, vsa_sparse_attn_fwd_fp8qk,
+                   vsa_quantize_fp8, vsa_sparse_attn_fwd_fp8qk, QKVOGrad, qkvo_grad, vsa_sparse_attn_bwd,
+                   vsa_sparse_attn_bwd_workspace_size, vsa_attention_bwd, vsa_attention_bwd_workspace_size,
                    vsa_gather_rows, vsa_kmeans, vsa_kmeans_workspace_size, vsa_scatter_rows, vsa_semantic_attention,
                    vsa_semantic_mask, vsa_semantic_mask_workspace_size, vsa_semantic_workspace_size)
 
@@ -89,6 +91,44 @@ class _HostPipelined:
 
 
 
+def _on(stream, device):
+    """Context in which `stream` (a torch stream or a raw handle; None: the current one) is current, so that
+    what is allocated in it belongs to the stream that uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream), device=device))
+
+
+def _no_capture(what: str):
+    # Autograd hands a leaf's gradient over on the stream on which the leaf's node was first used.  Under
+    # capture that can be a stream outside it, which ends the process; explicit calls have no such node.
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what} records a graph of autograd, which cannot be captured: capture the call and "
+                           f"its backward method instead")
+
+
+class _Attend(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, plan, q, k, v, kinds):
+        ctx.set_materialize_grads(False)
+        with torch.cuda.device(plan.device):
+            o, lse = plan(q, k, v, kinds=kinds)
+            ctx.plan = plan
+            ctx.save_for_backward(q, k, v, o, lse, plan.kinds.clone())
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_o):
+        if d_o is None:
+            return (None,) * 5
+        _no_capture("attend")
+        q, k, v, o, lse, kinds = ctx.saved_tensors
+        grads = ctx.plan.backward(d_o.contiguous(), q, k, v, o, lse, kinds=kinds)
+        return (None, *(g if need else None for g, need in zip(grads, ctx.needs_input_grad[1:4])), None)
+
+
 class SparseAttention(_HostPipelined):
     """One configured attention call over a B x H x (F x Hl x Wl) x d problem.
 
@@ -100,15 +140,23 @@ class SparseAttention(_HostPipelined):
              attention kernel instead of being permuted into copies (bf16, no cube dims).
     qk_fp8:  Q.K^T on e4m3 codes with one power-of-two scale per block; P.V stays bf16
              (bf16, d = 128, block 128).
+    with_grad: the plan also holds the workspace of the gradient (``backward``, ``attend``); the
+             call then always returns its log-sum-exp.  Not with qk_fp8.
+
+    A plan's workspaces serve one call at a time: order calls on different streams, and graphs
+    that captured them, before they run, or give each its own plan.
     """
 
     def __init__(self, B: int, H: int, F: int, Hl: int, Wl: int, d: int, block: int = 128, *,
                  dtype: torch.dtype = torch.bfloat16, select: str = "profile", w_s: Optional[int] = None,
                  w_t: Optional[int] = None, target: Optional[float] = None, topk: int = 0,
                  cube: Optional[Sequence[int]] = None, profile_frac: float = 0.01, scale: float = 0.0,
-                 with_lse: bool = False, layout_in_kernel: bool = False, qk_fp8: bool = False, device="cuda"):
+                 with_lse: bool = False, layout_in_kernel: bool = False, qk_fp8: bool = False,
+                 with_grad: bool = False, device="cuda"):
         if dtype not in _DTYPE:
             raise ValueError(f"unsupported dtype {dtype}")
+        if with_grad and qk_fp8:
+            raise ValueError("the e4m3 codes of qk_fp8 have no gradient")
         self.B, self.H, self.F, self.Hl, self.Wl, self.d, self.block = B, H, F, Hl, Wl, d, block
         self.N = F * Hl * Wl
         dev = torch.device(device)
@@ -139,7 +187,14 @@ class SparseAttention(_HostPipelined):
         self.kinds = torch.zeros(B * H, dtype=torch.uint8, device=self.device)
         self.mse = torch.zeros(B * H * 2, dtype=torch.float32, device=self.device)
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self.with_lse = with_lse
+        self.with_lse = with_lse or with_grad
+        self.with_grad = with_grad
+        if with_grad:
+            self.ws_bwd_bytes = vsa_attention_bwd_workspace_size(self.shape, self.params, _DTYPE[dtype])
+            if self.ws_bwd_bytes == 0:
+                raise VsaError(_lib.VSA_ERR_UNSUPPORTED, "vsa_attention_bwd_workspace_size")
+            self.ws_bwd = torch.empty(self.ws_bwd_bytes, dtype=torch.uint8, device=self.device)
+            self.kinds_bwd = torch.full((B * H,), VSA_CUBE, dtype=torch.uint8, device=self.device)
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None, kinds: Optional[torch.Tensor] = None, stream=None):
@@ -159,6 +214,49 @@ class SparseAttention(_HostPipelined):
         vsa_attention(qkvo(q, k, v, out, lse), _DTYPE[self.dtype], self.shape, self.params, self.select, self.kinds,
                       self.mse, self.ws, self.ws_bytes, self.err, stream)
         return (out, lse) if self.with_lse else out
+
+    def backward(self, d_o: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                 lse: torch.Tensor, kinds: Optional[torch.Tensor] = None, d_lse: Optional[torch.Tensor] = None,
+                 out: Optional[Sequence[torch.Tensor]] = None, stream=None):
+        """Gradients (dq, dk, dv) of a call of this plan, from its inputs, its outputs and the gradients
+        of those.  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
+        where another call comes between); they are not needed for select="cube".  Nothing else of the
+        call is kept: the masks are built again.  Asynchronous on ``stream``; can be captured."""
+        if not self.with_grad:
+            raise ValueError("the plan was made without with_grad=True")
+        shape = (self.B, self.H, self.N, self.d)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            if out is None:
+                out = tuple(torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(3))
+            if len(out) != 3:
+                raise ValueError("out is (dq, dk, dv)")
+            for t in (d_o, q, k, v, o, *out):
+                if t.dtype != self.dtype or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != shape:
+                    raise ValueError(f"contiguous {self.dtype} tensors of shape {shape} on {self.device} expected")
+            for t in (lse, d_lse):
+                if t is not None and (t.dtype != torch.float32 or t.device != self.device or not t.is_contiguous()
+                                      or tuple(t.shape) != shape[:3]):
+                    raise ValueError(f"lse and d_lse are contiguous float32 tensors of shape {shape[:3]} on {self.device}")
+            if self.select != VSA_SELECT_CUBE:
+                if kinds is None:
+                    raise ValueError("backward needs the kinds of the call")
+                if kinds.numel() != self.B * self.H:
+                    raise ValueError(f"{self.B * self.H} kinds expected")
+                self.kinds_bwd.copy_(kinds.reshape(-1).to(torch.uint8))
+            vsa_attention_bwd(qkvo_grad(q, k, v, o, d_o, lse, *out, d_lse=d_lse), _DTYPE[self.dtype], self.shape,
+                              self.params, self.kinds_bwd, self.ws_bwd, self.ws_bwd_bytes, self.err)
+        return tuple(out)
+
+    def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kinds: Optional[torch.Tensor] = None):
+        """The call as a differentiable function: o whose ``backward`` fills the gradients of q, k and v
+        (first derivatives; the masks count as constants).  Keeps q, k, v, o, the log-sum-exp and the
+        kinds for the gradient.  Where autograd records it is refused under graph capture: capture
+        the call itself and ``backward`` instead."""
+        if not self.with_grad:
+            raise ValueError("the plan was made without with_grad=True")
+        if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
+            _no_capture("attend")
+        return _Attend.apply(self, q, k, v, kinds)
 
     def device_error(self) -> int:
         return vsa_get_device_error(self.err)
@@ -269,5 +367,6 @@ __all__ = ["SparseAttention", "SemanticAttention", "attention", "SemParams", "ma
            "vsa_get_device_error", "vsa_layout_rows", "vsa_mask_workspace_size", "vsa_max_kv", "vsa_num_blocks",
            "vsa_pattern_window", "vsa_permute", "vsa_profile_heads", "vsa_profile_rows",
            "vsa_profile_workspace_size", "vsa_sparse_attn_fwd", "vsa_sparse_attn_fwd_natural", "vsa_unpermute",
-           "vsa_quantize_fp8", "vsa_sparse_attn_fwd_fp8qk", "VSA_SPATIAL", "VSA_TEMPORAL",
+           "vsa_quantize_fp8", "vsa_sparse_attn_fwd_fp8qk", "QKVOGrad", "qkvo_grad", "vsa_sparse_attn_bwd",
+           "vsa_sparse_attn_bwd_workspace_size", "vsa_attention_bwd", "vsa_attention_bwd_workspace_size", "VSA_SPATIAL", "VSA_TEMPORAL",
            "VSA_CUBE", "VSA_F32", "VSA_BF16", "VSA_SELECT_PROFILE", "VSA_SELECT_GIVEN", "VSA_SELECT_CUBE"]

@@ -56,6 +56,10 @@ class QKVO(ctypes.Structure):
                 ("lse", ctypes.c_void_p)]
 
 
+class QKVOGrad(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "d_o", "lse", "d_lse", "dq", "dk", "dv")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libvsa.so is not built ({LIB_PATH}); run `python block_sparse_attention_31_b200/build.py`")
@@ -89,6 +93,11 @@ def _load():
         "vsa_attention_host": (st, [P(HostBatch), i32, P(QKVO), i32, P(Shape), P(Params), i32, vp, vp, vp, sz, vp,
                                     vp, vp, vp]),
         "vsa_attention_workspace_layout": (st, [P(Shape), P(Params), i32, i32, P(sz), P(sz), P(sz), P(i32)]),
+        "vsa_sparse_attn_bwd_workspace_size": (sz, [P(Shape)]),
+        "vsa_sparse_attn_bwd": (st, [P(QKVOGrad), P(QKVOGrad), vp, vp, vp, i32, P(Shape), ctypes.c_float, vp, sz, vp,
+                                     vp]),
+        "vsa_attention_bwd_workspace_size": (sz, [P(Shape), P(Params), i32]),
+        "vsa_attention_bwd": (st, [P(QKVOGrad), i32, P(Shape), P(Params), vp, vp, sz, vp, vp]),
         "vsa_get_device_error": (st, [vp, vp, P(i32)]),
         "vsa_kmeans_workspace_size": (sz, [P(Shape), i32]),
         "vsa_kmeans": (st, [vp, P(Shape), i32, i32, vp, vp, vp, vp, vp, sz, vp, vp]),
@@ -299,6 +308,36 @@ def vsa_attention(io: QKVO, dtype: int, shape: Shape, params: Params, select: in
                   stream=None):
     _check(lib.vsa_attention(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), select, _ptr(kinds),
                              _ptr(mse), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention")
+
+
+# ---------------------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------------------
+
+def qkvo_grad(q, k, v, o, d_o, lse, dq, dk, dv, d_lse=None) -> QKVOGrad:
+    return QKVOGrad(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(d_lse), _ptr(dq), _ptr(dk),
+                    _ptr(dv))
+
+
+def vsa_sparse_attn_bwd_workspace_size(shape: Shape) -> int:
+    return int(lib.vsa_sparse_attn_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def vsa_sparse_attn_bwd(natural: QKVOGrad, permuted, kinds, kv_idx, kv_cnt, max_kv, shape: Shape, scale, ws, ws_bytes,
+                        err, stream=None):
+    _check(lib.vsa_sparse_attn_bwd(ctypes.byref(natural), ctypes.byref(permuted) if permuted is not None else None,
+                                   _ptr(kinds), _ptr(kv_idx), _ptr(kv_cnt), int(max_kv), ctypes.byref(shape),
+                                   float(scale), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)),
+           "vsa_sparse_attn_bwd")
+
+
+def vsa_attention_bwd_workspace_size(shape: Shape, params: Params, dtype: int) -> int:
+    return int(lib.vsa_attention_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(params), dtype))
+
+
+def vsa_attention_bwd(io: QKVOGrad, dtype: int, shape: Shape, params: Params, kinds, ws, ws_bytes, err, stream=None):
+    _check(lib.vsa_attention_bwd(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
+                                 _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention_bwd")
 
 
 def vsa_get_device_error(err, stream=None) -> int:

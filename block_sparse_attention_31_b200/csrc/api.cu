@@ -88,6 +88,23 @@ static bool on_device(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// on_device, and on the device that is current: a kernel launched on one device must not be given
+// another one's memory.
+static bool on_current_device(std::initializer_list<const void*> ptrs) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  for (const void* p : ptrs) {
+    if (p == nullptr) continue;
+    cudaPointerAttributes at;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    if (at.type != cudaMemoryTypeManaged && (at.type != cudaMemoryTypeDevice || at.device != dev)) return false;
+  }
+  return true;
+}
+
 // Validate the shape and derive the geometry.
 static vsa_status make_geom(const vsa_shape* s, Geom* g) {
   if (s == nullptr || g == nullptr) return VSA_ERR_INVALID_ARG;
@@ -529,6 +546,128 @@ vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo* natural, const uint8_t* d
 }
 
 // ---------------------------------------------------------------------------------------
+// Gradient of the attention
+// ---------------------------------------------------------------------------------------
+// Workspace of vsa_sparse_attn_bwd: one bitset and two terms per row of every query block.
+struct BwdLayout {
+  size_t off_bits, off_terms, bytes;
+};
+
+static BwdLayout bwd_layout(const Geom& g, int BH) {
+  BwdLayout L;
+  const size_t rows = static_cast<size_t>(BH) * g.nblk;
+  L.off_bits = 0;
+  L.off_terms = align256(rows * ((g.nblk + 31) / 32) * 4);
+  L.bytes = L.off_terms + align256(rows * g.block * 8);
+  return L;
+}
+
+static vsa_status check_grad(const vsa_qkvo_grad* t) {
+  if (t == nullptr) return VSA_ERR_INVALID_ARG;
+  for (const void* p : {t->q, t->k, t->v, t->o, t->d_o, static_cast<const void*>(t->lse),
+                        static_cast<const void*>(t->dq), static_cast<const void*>(t->dk),
+                        static_cast<const void*>(t->dv)})
+    if (p == nullptr || !aligned16(p)) return VSA_ERR_INVALID_ARG;
+  return VSA_OK;
+}
+
+static bool grad_on_device(const vsa_qkvo_grad* t) {
+  return on_current_device({t->q, t->k, t->v, t->o, t->d_o, t->lse, t->d_lse, t->dq, t->dk, t->dv});
+}
+
+static vsa_status encode_bwd_set(BwdMaps* m, const vsa_qkvo_grad* t, const Geom& g, int rows, int BH, int d) {
+  const struct {
+    CUtensorMap* map;
+    const void* p;
+  } all[] = {{&m->q, t->q}, {&m->k, t->k}, {&m->v, t->v}, {&m->g, t->d_o}, {&m->dq, t->dq}, {&m->dk, t->dk}, {&m->dv, t->dv}};
+  for (const auto& x : all)
+    if (encode_rows_map(x.map, x.p, d, rows, BH, g.block) != cudaSuccess) return VSA_ERR_CUDA;
+  return VSA_OK;
+}
+
+// The row terms from `rows` (O, dO, LSE: each head's layout, or natural order when by_token), then the
+// gradients of the two sets.  Arguments are checked by the callers.
+static vsa_status sparse_attn_bwd_impl(const vsa_qkvo_grad* natural, const vsa_qkvo_grad* permuted,
+                                       const vsa_qkvo_grad* rows, bool by_token, bool f32, const uint8_t* d_kind,
+                                       const int32_t* d_kv_idx, const int32_t* d_kv_cnt, int max_kv, const Geom& g,
+                                       int BH, int d, float scale, void* ws, int* d_err, cudaStream_t stream) {
+  vsa_status st;
+  BwdMaps nat, perm;
+  const int nat_rows = permuted != nullptr ? g.N : g.R;
+  if ((st = encode_bwd_set(&nat, natural, g, nat_rows, BH, d)) != VSA_OK) return st;
+  perm = nat;
+  if (permuted != nullptr && (st = encode_bwd_set(&perm, permuted, g, g.R, BH, d)) != VSA_OK) return st;
+  const BwdLayout L = bwd_layout(g, BH);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  BwdPrep p{};
+  p.kinds = d_kind;
+  p.kv_idx = d_kv_idx;
+  p.kv_cnt = d_kv_cnt;
+  p.o_nat = rows->o;
+  p.do_nat = rows->d_o;
+  p.lse_nat = rows->lse;
+  p.dlse_nat = rows->d_lse;
+  if (permuted != nullptr) {
+    p.o_perm = permuted->o;
+    p.do_perm = permuted->d_o;
+    p.lse_perm = permuted->lse;
+    p.dlse_perm = permuted->d_lse;
+  }
+  p.rbits = reinterpret_cast<uint32_t*>(w + L.off_bits);
+  p.terms = reinterpret_cast<float*>(w + L.off_terms);
+  p.err = d_err;
+  p.BH = BH;
+  p.d = d;
+  p.max_kv = max_kv;
+  p.has_perm = permuted != nullptr;
+  p.nat_rows = nat_rows;
+  p.by_token = by_token;
+  p.f32 = f32;
+  p.g = g;
+  BwdArgs a{};
+  a.kinds = d_kind;
+  a.rbits = p.rbits;
+  a.terms = p.terms;
+  a.err = d_err;
+  a.nat_dq = natural->dq;
+  a.nat_dk = natural->dk;
+  a.nat_dv = natural->dv;
+  a.BH = BH;
+  a.has_perm = permuted != nullptr;
+  a.nat_rows = nat_rows;
+  a.scale_log2 = scale_log2_of(scale, d);
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d));
+  a.g = g;
+  return launch_sparse_attn_bwd(nat, perm, p, a, d, stream) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape* shape) {
+  Geom g;
+  if (make_geom(shape, &g) != VSA_OK || !sparse_attn_bwd_fits(g, shape->B * shape->H)) return 0;
+  return bwd_layout(g, shape->B * shape->H).bytes;
+}
+
+vsa_status vsa_sparse_attn_bwd(const vsa_qkvo_grad* natural, const vsa_qkvo_grad* permuted, const uint8_t* d_kind,
+                               const int32_t* d_kv_idx, const int32_t* d_kv_cnt, int max_kv, const vsa_shape* shape,
+                               float scale, void* ws, size_t ws_bytes, int* d_err, cudaStream_t stream) {
+  Geom g;
+  vsa_status st = make_geom(shape, &g);
+  if (st != VSA_OK) return st;
+  if ((st = check_grad(natural)) != VSA_OK) return st;
+  if (permuted != nullptr && (st = check_grad(permuted)) != VSA_OK) return st;
+  if (!d_kind || !d_kv_idx || !d_kv_cnt || !d_err || max_kv <= 0 || !(scale >= 0.f) || !ws || !aligned16(ws))
+    return VSA_ERR_INVALID_ARG;
+  const int BH = shape->B * shape->H;
+  if (!sparse_attn_bwd_fits(g, BH)) return VSA_ERR_UNSUPPORTED;
+  if (ws_bytes < bwd_layout(g, BH).bytes) return VSA_ERR_WORKSPACE;
+  if (!grad_on_device(natural) || (permuted != nullptr && !grad_on_device(permuted)) ||
+      !on_current_device({d_kind, d_kv_idx, d_kv_cnt, ws, d_err}))
+    return VSA_ERR_INVALID_ARG;
+  return sparse_attn_bwd_impl(natural, permuted, natural, false, false, d_kind, d_kv_idx, d_kv_cnt, max_kv, g, BH,
+                              shape->d, scale, ws, d_err, stream);
+}
+
+// ---------------------------------------------------------------------------------------
 // Semantic-aware permutation ("Sparse VideoGen2" page, abstract)
 // ---------------------------------------------------------------------------------------
 // Shapes of the semantic path: no cube dims (every head has N rows).
@@ -877,6 +1016,96 @@ vsa_status vsa_attention(const vsa_qkvo* io, vsa_dtype dtype, const vsa_shape* s
   if (st != VSA_OK) return st;
   // 5. back to natural order
   return vsa_unpermute(po, plse, io->o, dtype, io->lse, d_kind, shape, d_err, stream);
+}
+
+// Workspace of vsa_attention_bwd: the masks, the permuted q, k, v, dO, dq, dk, dv, the mask and the
+// gradient kernels' scratch.
+struct AttnBwdLayout {
+  size_t off_bits, off_idx, off_cnt, off_t[7], off_mask, mask_bytes, off_bwd, bytes;
+  int max_kv;
+};
+
+static vsa_status attention_bwd_layout(const vsa_shape* shape, const vsa_params* params, vsa_dtype dtype,
+                                       AttnBwdLayout* L) {
+  Geom g;
+  vsa_status st = make_geom(shape, &g);
+  if (st != VSA_OK) return st;
+  if (params == nullptr || !(params->scale >= 0.f)) return VSA_ERR_INVALID_ARG;
+  if (dtype != VSA_F32 && dtype != VSA_BF16) return VSA_ERR_INVALID_ARG;
+  if (params->qk_fp8 != 0) return VSA_ERR_UNSUPPORTED;  // the codes have no gradient
+  const int BH = shape->B * shape->H;
+  if (!sparse_attn_bwd_fits(g, BH)) return VSA_ERR_UNSUPPORTED;
+  if ((st = vsa_max_kv(shape, params, &L->max_kv)) != VSA_OK) return st;
+  L->max_kv = std::max(L->max_kv, 1);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  const size_t lists = static_cast<size_t>(BH) * g.nblk;
+  L->off_bits = take(lists * ((g.nblk + 31) / 32) * 4);
+  L->off_idx = take(lists * L->max_kv * 4);
+  L->off_cnt = take(lists * 4);
+  for (size_t& t : L->off_t) t = take(static_cast<size_t>(BH) * g.R * shape->d * 2);
+  L->mask_bytes = vsa_mask_workspace_size(shape, params);
+  L->off_mask = take(L->mask_bytes);
+  L->off_bwd = take(bwd_layout(g, BH).bytes);
+  L->bytes = off;
+  return VSA_OK;
+}
+
+size_t vsa_attention_bwd_workspace_size(const vsa_shape* shape, const vsa_params* params, vsa_dtype dtype) {
+  AttnBwdLayout L;
+  return attention_bwd_layout(shape, params, dtype, &L) == VSA_OK ? L.bytes : 0;
+}
+
+vsa_status vsa_attention_bwd(const vsa_qkvo_grad* io, vsa_dtype dtype, const vsa_shape* shape,
+                             const vsa_params* params, const uint8_t* d_kind, void* ws, size_t ws_bytes, int* d_err,
+                             cudaStream_t stream) {
+  AttnBwdLayout L;
+  vsa_status st = attention_bwd_layout(shape, params, dtype, &L);
+  if (st != VSA_OK) return st;
+  if ((st = check_grad(io)) != VSA_OK) return st;
+  if (!d_kind || !ws || !d_err || !aligned16(ws)) return VSA_ERR_INVALID_ARG;
+  if (ws_bytes < L.bytes) return VSA_ERR_WORKSPACE;
+  if (!grad_on_device(io) || !on_current_device({d_kind, ws, d_err})) return VSA_ERR_INVALID_ARG;
+  Geom g;
+  make_geom(shape, &g);
+  const int BH = shape->B * shape->H;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(w + L.off_bits);
+  int32_t* kv_idx = reinterpret_cast<int32_t*>(w + L.off_idx);
+  int32_t* kv_cnt = reinterpret_cast<int32_t*>(w + L.off_cnt);
+  // 1. each head's layout of q, k, v and dO
+  vsa_qkvo_grad set{};
+  void* t[7];
+  for (int i = 0; i < 7; ++i) t[i] = w + L.off_t[i];
+  const void* src[4] = {io->q, io->k, io->v, io->d_o};
+  for (int i = 0; i < 4; ++i)
+    if ((st = vsa_permute(src[i], dtype, t[i], d_kind, shape, d_err, stream)) != VSA_OK) return st;
+  set.q = t[0];
+  set.k = t[1];
+  set.v = t[2];
+  set.d_o = t[3];
+  set.dq = t[4];
+  set.dk = t[5];
+  set.dv = t[6];
+  // 2. the call's masks
+  if ((st = vsa_build_mask(d_kind, t[0], t[1], shape, params, bits, kv_idx, kv_cnt, L.max_kv, w + L.off_mask,
+                           L.mask_bytes, d_err, stream)) != VSA_OK)
+    return st;
+  // 3. gradients: spatial heads in place for bf16, everything else through the copies
+  const bool f32 = dtype == VSA_F32;
+  if ((st = sparse_attn_bwd_impl(f32 ? &set : io, f32 ? nullptr : &set, io, true, f32, d_kind, kv_idx, kv_cnt, L.max_kv,
+                                 g, BH, shape->d, params->scale, w + L.off_bwd, d_err, stream)) != VSA_OK)
+    return st;
+  // 4. back to natural order
+  void* dst[3] = {io->dq, io->dk, io->dv};
+  for (int i = 0; i < 3; ++i)
+    if ((st = vsa_unpermute(t[4 + i], nullptr, dst[i], dtype, nullptr, d_kind, shape, d_err, stream)) != VSA_OK)
+      return st;
+  return VSA_OK;
 }
 
 vsa_status vsa_attention_host(const vsa_host_batch* host, int n, const vsa_qkvo* sets, vsa_dtype dtype,

@@ -1,0 +1,642 @@
+// attn_bwd.cu -- gradient of the block-sparse attention (vsa_sparse_attn_bwd) for sm_100a.
+//
+// With P = exp(scale * Q K^T - lse) on the kept block pairs (0 elsewhere, and on rows whose lse
+// is -inf) and delta_i = sum_d dO_id O_id - dlse_i:
+//
+//   dV = P^T dO     dP = dO V^T     dS = P o (dP - delta)     dQ = scale dS K     dK = scale dS^T Q
+//
+// P is recomputed from the forward call's log-sum-exp; nothing of size N x N is stored.
+//
+// Two launches.  bwd_prep_kernel turns each row's lse and delta into the two terms the main
+// kernel adds (-lse * log2 e and -delta, -inf and 0 for rows that see nothing) and validates the
+// key lists into one bitset per query block.  sparse_attn_bwd_kernel then runs two kinds of CTA:
+//
+//   key CTAs    own one key block: they walk the query blocks that keep it (its column of the
+//               bitset) and accumulate dV and dK in TMEM.  S^T = K Q^T and dP^T = V dO^T have the
+//               keys as TMEM lanes, so that P^T and dS^T are written over them as packed bf16 and
+//               read from TMEM as the A operands of dV += P^T dO and dK += dS^T Q.
+//   query CTAs  own one query block: they walk its kept key blocks and accumulate dQ; S = Q K^T
+//               and dP = dO V^T have the queries as lanes, dS is written over S.
+//
+// S and dP are computed twice (7 products instead of 5) so that every gradient has one owner:
+// no atomics, no fp32 copy of dQ in memory, the same bits on every run.
+//
+// Each CTA: 384 threads in three warpgroups (registers rebalanced as in the forward kernel).
+//   warps 0-3 / 4-7  one lane (row of S) per thread, the first / second half of its columns:
+//                    p = exp2(s * scale * log2 e - lse * log2 e) in fp32, packed to bf16 for the
+//                    dV product, kept in registers in fp32 for dS = p * (dP - delta)
+//   warp 8 / 10      TMA producers of the two rings (X: Q or K with the rows' terms; Y: dO or V)
+//   warp 9           the tcgen05 issuer (one lane); owns TMEM
+// P and dS are rounded to bf16 because both operands of the tensor product have one type; every
+// sum (S, dP, dV, dK, dQ) is held in fp32.
+//
+// Operand tiles use the 128-byte swizzle as in the forward kernel; every wait is bounded, and on a
+// timeout the CTA drains its copies and MMAs, frees TMEM and returns.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace vsa {
+
+namespace {
+
+constexpr int kBwdThreads = 384;
+constexpr int kWarpX = 8, kWarpMma = 9, kWarpY = 10;
+constexpr int kBM = 128;
+constexpr int kRegsSoftmax = 208, kRegsCtl = 88;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl == 384 * 168, "register split must equal the launch total");
+constexpr int kPolyPairs8 = 1;  // probability pairs in 8 whose exponentials run on the FMA pipe
+
+template <int D, int BN>
+struct BwdCfg {
+  static constexpr int NX = D * BN == 128 * 128 ? 3 : 4;  // ring stages of X (Q or K)
+  static constexpr int NY = D * BN == 128 * 128 ? 1 : 2;  // ring stages of Y (dO or V)
+  static constexpr int A_BYTES = kBM * D * 2;             // a resident tile (M = 128 lanes, BN rows loaded)
+  static constexpr int T_BYTES = BN * D * 2;              // a ring tile
+  static constexpr int ST_BYTES = 2 * BN * 4;             // the rows' two terms of a block
+  static constexpr int PANELS = D / 64;
+  static constexpr int OFF_A0 = 0;                        // K (key CTA) or Q (query CTA)
+  static constexpr int OFF_A1 = OFF_A0 + A_BYTES;         // V or dO
+  static constexpr int OFF_X = OFF_A1 + A_BYTES;
+  static constexpr int OFF_Y = OFF_X + NX * T_BYTES;
+  static constexpr int OFF_ST = OFF_Y + NY * T_BYTES;
+  static constexpr int OFF_BAR = OFF_ST + NX * ST_BYTES;
+  static constexpr int NBAR = 32;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_BITS = OFF_MISC + 64;
+  // TMEM columns.  Key CTA: S, dP, dV, dK.  Query CTA: S of two blocks, dP, dQ.
+  static constexpr int TM_S = 0;
+  static constexpr int TM_DP_K = BN, TM_DV = 2 * BN, TM_DK = 2 * BN + D;
+  static constexpr int TM_DP_Q = 2 * BN, TM_DQ = 3 * BN;
+  static constexpr int TM_USED = (2 * BN + 2 * D) > (3 * BN + D) ? (2 * BN + 2 * D) : (3 * BN + D);
+  static constexpr int TM_COLS = TM_USED <= 256 ? 256 : 512;
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(kBM, BN, false, false);
+  static constexpr uint32_t IDESC_G = idesc_bf16_f32(kBM, D, false, true);
+  static int smem_bytes(int nwords) { return OFF_BITS + 4 * nwords + 1024; }
+};
+
+enum {
+  B_A0 = 0,
+  B_A1 = 1,
+  B_FULL_X = 2,    // +stage (up to 4)
+  B_REL_X = 6,     // +stage
+  B_FULL_Y = 10,   // +stage (up to 4)
+  B_REL_Y = 14,    // +stage
+  B_FULL_ST = 18,  // +stage of X
+  B_S = 22,        // +buffer
+  B_DP = 24,
+  B_P = 25,
+  B_DS = 26,
+  B_FINAL = 27,
+};
+
+// The set bits of a bitset in ascending order.
+struct BitWalk {
+  const uint32_t* w;
+  int at;
+  uint32_t cur;
+  __device__ explicit BitWalk(const uint32_t* words) : w(words), at(0), cur(words[0]) {}
+  __device__ int next() {  // only called while a bit is left
+    while (cur == 0u) cur = w[++at];
+    const int b = at * 32 + __ffs(cur) - 1;
+    cur &= cur - 1u;
+    return b;
+  }
+};
+
+// p = 2^x of a packed pair; pair c of a row's half.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int c) {
+  if ((c & 7) >= 8 - kPolyPairs8) return exp2_poly2(x);
+  float x0, x1;
+  f2_split(x, x0, x1);
+  return f2_make(fast_exp2(x0), fast_exp2(x1));
+}
+
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+  float x0, x1;
+  f2_split(x, x0, x1);
+  return pack_bf16x2(x0, x1);
+}
+
+// N consecutive TMEM columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+#pragma unroll
+  for (int c = 0; c < N / 32; ++c) tmem_ld32_async(taddr + c * 32, r + c * 32);
+  tmem_wait_ld();
+  reg_fence<N>(r);
+}
+
+// One lane's D (or D/2) accumulator columns -> bf16 rows of the swizzled staging tile.
+template <int BN, int COLS>
+__device__ __forceinline__ void stage_rows(uint8_t* stage, uint32_t taddr, int col0, int row, bool live, bool have,
+                                           float scale) {
+#pragma unroll 1
+  for (int c = 0; c < COLS / 32; ++c) {
+    float o[32];
+    tmem_ld32(taddr + c * 32, o);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] = have && live ? o[x] * scale : 0.f;
+    if (row < BN) {
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint4 v4;
+        v4.x = pack_bf16x2(o[q4 * 8 + 0], o[q4 * 8 + 1]);
+        v4.y = pack_bf16x2(o[q4 * 8 + 2], o[q4 * 8 + 3]);
+        v4.z = pack_bf16x2(o[q4 * 8 + 4], o[q4 * 8 + 5]);
+        v4.w = pack_bf16x2(o[q4 * 8 + 6], o[q4 * 8 + 7]);
+        const int col = col0 + c * 32 + q4 * 8;
+        const int dc = col >> 6, cc = (col & 63) >> 3;
+        *reinterpret_cast<uint4*>(stage + dc * (BN * 128) + row * 128 + ((cc ^ (row & 7)) << 4)) = v4;
+      }
+    }
+  }
+}
+
+// kKey: a key CTA (dK, dV of block `blk`); else a query CTA (dQ of block `blk`).
+template <int D, int BN, bool kKey>
+__device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, const BwdArgs& a, int bh, int blk,
+                                        uint8_t* smem_raw) {
+  using C = BwdCfg<D, BN>;
+  constexpr int H = BN / 2;  // columns per thread
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw_u32);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);  // [0] TMEM base, [1] abort flag
+  volatile int* abort_flag = misc + 1;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Geom& g = a.g;
+  const int nwords = (g.nblk + 31) >> 5;
+  const int kind = a.kinds[bh];
+
+  if (kind > kCube || (kind == kCube && g.ncubes == 0)) {
+    // unknown layout: this block's rows of the natural-order gradients become zeros
+    if (tid == 0 && blk == 0) atomicOr(a.err, kDevErrKind);
+    const int r0 = blk * BN, r1 = min(r0 + BN, a.nat_rows);
+    for (int x = tid; x < (r1 - r0) * (D / 8); x += kBwdThreads) {
+      const size_t at = (static_cast<size_t>(bh) * a.nat_rows + r0) * (D / 8) + x;
+      if (kKey) {
+        static_cast<uint4*>(a.nat_dk)[at] = make_uint4(0, 0, 0, 0);
+        static_cast<uint4*>(a.nat_dv)[at] = make_uint4(0, 0, 0, 0);
+      } else {
+        static_cast<uint4*>(a.nat_dq)[at] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  const int rows = layout_rows(g, kind);
+  const int nb_head = (rows + BN - 1) / BN;
+  if (blk >= nb_head) return;
+  const BwdMaps* m = a.has_perm && kind != kSpatial ? mp : mn;
+
+  // ---- the blocks this CTA walks, barriers, TMEM ----
+  const uint32_t* rbits = a.rbits + static_cast<size_t>(bh) * g.nblk * nwords;
+  if (kKey) {
+    for (int w = warp; w < nwords; w += kBwdThreads / 32) {
+      const int r = w * 32 + lane;
+      const bool keeps = r < nb_head && ((rbits[static_cast<size_t>(r) * nwords + (blk >> 5)] >> (blk & 31)) & 1u);
+      const uint32_t word = __ballot_sync(0xffffffffu, keeps);
+      if (lane == 0) bits[w] = word;
+    }
+  } else {
+    for (int w = tid; w < nwords; w += kBwdThreads) bits[w] = rbits[static_cast<size_t>(blk) * nwords + w];
+  }
+  bool stop = false;
+  if (tid == 0) {
+    stop = (*reinterpret_cast<volatile int*>(a.err) & kDevErrTimeout) != 0;
+    mbar_init(bar(B_A0), 1);
+    mbar_init(bar(B_A1), 1);
+    for (int s = 0; s < C::NX; ++s) {
+      mbar_init(bar(B_FULL_X + s), 1);
+      mbar_init(bar(B_REL_X + s), 1);
+      mbar_init(bar(B_FULL_ST + s), 1);
+    }
+    for (int s = 0; s < C::NY; ++s) {
+      mbar_init(bar(B_FULL_Y + s), 1);
+      mbar_init(bar(B_REL_Y + s), 1);
+    }
+    mbar_init(bar(B_S), 1);
+    mbar_init(bar(B_S + 1), 1);
+    mbar_init(bar(B_DP), 1);
+    mbar_init(bar(B_P), 256);
+    mbar_init(bar(B_DS), 256);
+    mbar_init(bar(B_FINAL), 1);
+    misc[1] = 0;
+    mbar_init_fence();
+  }
+  if (__syncthreads_or(stop)) return;
+  if (warp == kWarpMma) {
+    tmem_alloc(sbase + C::OFF_MISC, C::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  int U = 0;
+  for (int w = lane; w < nwords; w += 32) U += __popc(bits[w]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) U += __shfl_xor_sync(0xffffffffu, U, off);
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kRegsCtl>();
+    if (warp == kWarpX || warp == kWarpY) {
+      // ================= TMA producers =================
+      if (lane == 0 && U > 0) {
+        const bool isx = warp == kWarpX;
+        // resident tile
+        const CUtensorMap* ta = kKey ? (isx ? &m->k : &m->v) : (isx ? &m->q : &m->g);
+        const uint32_t dst_a = sbase + (isx ? C::OFF_A0 : C::OFF_A1), bar_a = bar(isx ? B_A0 : B_A1);
+        mbar_arrive_expect_tx(bar_a, C::T_BYTES);
+#pragma unroll
+        for (int c = 0; c < C::PANELS; ++c) tma_load_3d(dst_a + c * kBM * 128, ta, bar_a, c * 64, blk * BN, bh);
+        // ring
+        const CUtensorMap* tr = kKey ? (isx ? &m->q : &m->g) : (isx ? &m->k : &m->v);
+        const int ns = isx ? C::NX : C::NY;
+        const int full0 = isx ? B_FULL_X : B_FULL_Y, rel0 = isx ? B_REL_X : B_REL_Y;
+        const uint32_t dst_r = sbase + (isx ? C::OFF_X : C::OFF_Y);
+        BitWalk walk(bits);
+        int st = 0, ph = 1, issued = 0;  // ph: parity of the release to wait for
+        for (int n = 0; n < U; ++n) {
+          const int b = walk.next();
+          if (n >= ns && !mbar_wait(bar(rel0 + st), ph, abort_flag, a.err)) break;
+          mbar_arrive_expect_tx(bar(full0 + st), C::T_BYTES);
+#pragma unroll
+          for (int c = 0; c < C::PANELS; ++c)
+            tma_load_3d(dst_r + st * C::T_BYTES + c * BN * 128, tr, bar(full0 + st), c * 64, b * BN, bh);
+          if (kKey && isx) {
+            mbar_arrive_expect_tx(bar(B_FULL_ST + st), C::ST_BYTES);
+            bulk_load(sbase + C::OFF_ST + st * C::ST_BYTES,
+                      a.terms + (static_cast<size_t>(bh) * g.nblk + b) * (2 * BN), C::ST_BYTES, bar(B_FULL_ST + st));
+          }
+          issued = n + 1;
+          if (++st == ns) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (*abort_flag) {  // every copy this thread issued lands before the CTA exits
+          mbar_wait_drain(bar_a, 0, a.err);
+          for (int s = 0; s < ns; ++s) {
+            int last = -1;
+            for (int n = s; n < issued; n += ns) last = n;
+            if (last < 0) continue;
+            mbar_wait_drain(bar(full0 + s), (last / ns) & 1, a.err);
+            if (kKey && isx) mbar_wait_drain(bar(B_FULL_ST + s), (last / ns) & 1, a.err);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ================= tcgen05 issuer =================
+      if (lane == 0 && U > 0) {
+        const uint64_t da0 = sdesc_sw128(sbase + C::OFF_A0, 16, 1024), da1 = sdesc_sw128(sbase + C::OFF_A1, 16, 1024);
+        // ring tiles as K-major (S, dP) and MN-major (gradient) B operands
+        const uint64_t dxk = sdesc_sw128(sbase + C::OFF_X, 16, 1024);
+        const uint64_t dyk = sdesc_sw128(sbase + C::OFF_Y, 16, 1024);
+        const uint64_t dxm = sdesc_sw128(sbase + C::OFF_X, BN * 128, 1024);
+        const uint64_t dym = sdesc_sw128(sbase + C::OFF_Y, BN * 128, 1024);
+        constexpr uint64_t kStage = C::T_BYTES / 16;
+        bool ok = true;
+        int xs = 0, xp = 0, ys = 0, yp = 0;  // next X and Y stage to be read by S and dP
+        int xr = 0, yr = 0;                  // stage of the gradient product
+        auto wait = [&](int b, int parity) {
+          if (ok && !mbar_wait(bar(b), parity, abort_flag, a.err)) ok = false;
+          return ok;
+        };
+        // D[lanes, BN] = A (resident) * ring tile^T
+        auto product = [&](uint32_t d_tm, uint64_t da, uint64_t db) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ss(d_tm, da + static_cast<uint64_t>(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) / 16),
+                      db + static_cast<uint64_t>(((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16), C::IDESC_S,
+                      kk > 0 ? 1u : 0u);
+        };
+        // acc[lanes, D] += packed bf16 (TMEM, two halves of the columns) * ring tile
+        auto accumulate = [&](uint32_t d_tm, uint32_t a_tm, uint64_t db, bool first) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            tc_mma_ts(d_tm, a_tm + (kk < BN / 32 ? kk * 8 : H + (kk - BN / 32) * 8),
+                      db + static_cast<uint64_t>(kk * 16 * 128 / 16), C::IDESC_G, first && kk == 0 ? 0u : 1u);
+        };
+        auto next_s = [&](int buf) {
+          if (!wait(B_FULL_X + xs, xp)) return;
+          product(tmem + C::TM_S + buf * BN, da0, dxk + xs * kStage);
+          tc_commit(bar(B_S + buf));
+          if (++xs == C::NX) {
+            xs = 0;
+            xp ^= 1;
+          }
+        };
+        auto next_dp = [&]() {
+          if (!wait(B_FULL_Y + ys, yp)) return;
+          product(tmem + (kKey ? C::TM_DP_K : C::TM_DP_Q), da1, dyk + ys * kStage);
+          tc_commit(bar(B_DP));
+          if (!kKey) tc_commit(bar(B_REL_Y + ys));
+          if (++ys == C::NY) {
+            ys = 0;
+            yp ^= 1;
+          }
+        };
+        wait(B_A0, 0);
+        if (ok) next_s(0);
+        if (ok) wait(B_A1, 0);
+        if (ok) next_dp();
+        if constexpr (kKey) {
+          for (int n = 0; ok && n < U; ++n) {
+            if (!wait(B_P, n & 1)) break;
+            accumulate(tmem + C::TM_DV, tmem + C::TM_S, dym + yr * kStage, n == 0);
+            tc_commit(bar(B_REL_Y + yr));
+            if (++yr == C::NY) yr = 0;
+            if (n + 1 < U) next_s(0);
+            if (!wait(B_DS, n & 1)) break;
+            accumulate(tmem + C::TM_DK, tmem + C::TM_DP_K, dxm + xr * kStage, n == 0);
+            tc_commit(bar(B_REL_X + xr));
+            if (++xr == C::NX) xr = 0;
+            if (n + 1 < U) next_dp();
+          }
+        } else {
+          if (ok && U > 1) next_s(1);
+          for (int n = 0; ok && n < U; ++n) {
+            if (!wait(B_DS, n & 1)) break;
+            if (n + 1 < U) next_dp();
+            if (!ok) break;
+            accumulate(tmem + C::TM_DQ, tmem + C::TM_S + (n & 1) * BN, dxm + xr * kStage, n == 0);
+            tc_commit(bar(B_REL_X + xr));
+            if (++xr == C::NX) xr = 0;
+            if (n + 2 < U) next_s(n & 1);
+          }
+        }
+        // all MMAs of this thread complete before the accumulators are read or TMEM is released
+        tc_commit(bar(B_FINAL));
+        mbar_wait_drain(bar(B_FINAL), 0, a.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ================= probabilities and dS: one lane per thread, half of the columns =================
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int half = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int slot = blk * BN + row;
+    const bool live = row < BN && slot < rows && token_of_slot(g, kind, slot) >= 0;
+    const uint64_t sl2 = f2_make(a.scale_log2, a.scale_log2);
+    uint64_t nl_row = 0, nd_row = 0;  // query CTA: this row's terms
+    if (!kKey) {
+      const float* t = a.terms + (static_cast<size_t>(bh) * g.nblk + blk) * (2 * BN);
+      const float nl = row < BN ? t[row] : -INFINITY, nd = row < BN ? t[BN + row] : 0.f;
+      nl_row = f2_make(nl, nl);
+      nd_row = f2_make(nd, nd);
+    }
+    bool ok = true;
+    BitWalk walk(bits);
+    int st = 0, ph = 0;
+    for (int n = 0; n < U; ++n) {
+      const int b = walk.next();
+      const int buf = kKey ? 0 : (n & 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + buf), kKey ? (n & 1) : ((n >> 1) & 1), abort_flag, a.err));
+      if (ok && kKey) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL_ST + st), ph, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = t_lane + C::TM_S + buf * BN + half * H;
+      const uint32_t t_dp = t_lane + (kKey ? C::TM_DP_K : C::TM_DP_Q) + half * H;
+      const uint64_t* terms = reinterpret_cast<const uint64_t*>(smem + C::OFF_ST + st * C::ST_BYTES) + half * (H / 2);
+      uint64_t p[H / 2];
+      {
+        uint32_t r[H];
+        tmem_ld_cols<H>(t_s, r);
+        if (!kKey && !block_full(g, kind, b)) {  // key columns that hold no token (ragged tail, cube padding)
+#pragma unroll
+          for (int w = 0; w < H / 32; ++w) {
+            const uint32_t vb =
+                __ballot_sync(0xffffffffu, token_of_slot(g, kind, b * BN + half * H + w * 32 + lane) >= 0);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) r[w * 32 + x] = ((vb >> x) & 1u) ? r[w * 32 + x] : 0xff800000u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < H / 2; ++c)
+          p[c] = exp2_pair(f2_fma(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sl2,
+                                  kKey ? terms[c] : nl_row),
+                           c);
+      }
+      if constexpr (kKey) {
+        uint32_t pk[H / 2];
+#pragma unroll
+        for (int c = 0; c < H / 2; ++c) pk[c] = pack_pair(p[c]);
+        tmem_st_cols<H / 2>(t_s, pk);
+        tc_fence_before();
+        mbar_arrive(bar(B_P));
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DP), n & 1, abort_flag, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      {
+        uint32_t r[H];
+        tmem_ld_cols<H>(t_dp, r);
+        uint32_t pk[H / 2];
+#pragma unroll
+        for (int c = 0; c < H / 2; ++c)
+          pk[c] = pack_pair(f2_mul(p[c], f2_add(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])),
+                                                kKey ? terms[BN / 2 + c] : nd_row)));
+        tmem_st_cols<H / 2>(kKey ? t_dp : t_s, pk);
+      }
+      tc_fence_before();
+      mbar_arrive(bar(B_DS));
+      if (++st == C::NX) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    // ---- epilogue: accumulators -> bf16 -> swizzled shared memory (over the resident tiles) -> TMA store ----
+    if (ok && U > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FINAL), 0, abort_flag, a.err));
+      tc_fence_after();
+    }
+    const bool have = ok && U > 0;
+    if constexpr (kKey) {
+      // warps 0-3 write dV over V's tile, warps 4-7 dK over K's
+      const int off = half ? C::OFF_A0 : C::OFF_A1;
+      stage_rows<BN, D>(smem + off, t_lane + (half ? C::TM_DK : C::TM_DV), 0, row, live, have, half ? a.scale : 1.f);
+      fence_proxy_async_smem();
+      named_barrier_sync(1 + half, 128);
+      if (quad == 2 && lane == 0) {
+#pragma unroll
+        for (int c = 0; c < C::PANELS; ++c)
+          tma_store_3d(half ? &m->dk : &m->dv, sbase + off + c * BN * 128, c * 64, blk * BN, bh);
+        tma_store_commit();
+        tma_store_wait_all();
+      }
+    } else {
+      stage_rows<BN, D / 2>(smem + C::OFF_A0, t_lane + C::TM_DQ + half * (D / 2), half * (D / 2), row, live, have,
+                            a.scale);
+      fence_proxy_async_smem();
+      named_barrier_sync(1, 256);
+      if (warp == 2 && lane == 0) {
+#pragma unroll
+        for (int c = 0; c < C::PANELS; ++c)
+          tma_store_3d(&m->dq, sbase + C::OFF_A0 + c * BN * 128, c * 64, blk * BN, bh);
+        tma_store_commit();
+        tma_store_wait_all();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, C::TM_COLS);
+}
+
+template <int D, int BN>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    sparse_attn_bwd_kernel(const __grid_constant__ BwdMaps mn, const __grid_constant__ BwdMaps mp,
+                           const __grid_constant__ BwdArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const int per = a.BH * a.g.nblk;
+  const int at = static_cast<int>(blockIdx.x);
+  const int i = at < per ? at : at - per;
+  const int bh = i / a.g.nblk, blk = i - bh * a.g.nblk;
+  if (at < per) bwd_cta<D, BN, true>(&mn, &mp, a, bh, blk, smem_raw);
+  else bwd_cta<D, BN, false>(&mn, &mp, a, bh, blk, smem_raw);
+}
+
+// ---------------------------------------------------------------------------------------
+// Row terms and row bitsets
+// ---------------------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+    s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
+  }
+  return s;
+}
+
+// Eight values of a row as bf16 (fp32 rows round to nearest even, as the permuted copies do).
+__device__ __forceinline__ uint4 load8(const void* p, size_t at, bool f32) {
+  if (!f32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+  const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  const float4 a = __ldg(q), b = __ldg(q + 1);
+  return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
+
+// CTAs [0, mask_ctas): one warp per query block checks its list (ascending, in range, count within
+// max_kv) and writes it as bits; a bad list sets the error bit and becomes empty.
+// The others: d / 8 threads per slot of a head's padded rows; the two terms of the slot's row.
+__global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a) {
+  const Geom& g = a.g;
+  if (static_cast<int>(blockIdx.x) < a.mask_ctas) {
+    const int nwords = (g.nblk + 31) >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * (kPrepThreads / 32) + warp;
+    if (row >= static_cast<long long>(a.BH) * g.nblk) return;
+    const int bh = static_cast<int>(row / g.nblk), i = static_cast<int>(row - static_cast<long long>(bh) * g.nblk);
+    const int kind = a.kinds[bh];
+    const int nb = kind > kCube ? 0 : (layout_rows(g, kind) + g.block - 1) / g.block;
+    const int32_t* list = a.kv_idx + row * a.max_kv;
+    uint32_t* out = a.rbits + row * nwords;
+    const int cnt = i < nb ? a.kv_cnt[row] : 0;
+    bool bad = cnt < 0 || cnt > a.max_kv;
+    if (!bad)
+      for (int j = lane; j < cnt; j += 32) {
+        const int kb = list[j];
+        if (kb < 0 || kb >= nb || (j > 0 && list[j - 1] >= kb)) bad = true;
+      }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad && lane == 0) atomicOr(a.err, kDevErrKvRange);
+    const int n = bad ? 0 : cnt;
+    // word w holds the listed blocks in [32 w, 32 w + 32): each lane finds them by binary search
+    for (int w = lane; w < nwords; w += 32) {
+      int lo = 0, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] < w * 32) lo = mid + 1;
+        else hi = mid;
+      }
+      uint32_t word = 0u;
+      for (int j = lo; j < n && list[j] < w * 32 + 32; ++j) word |= 1u << (list[j] & 31);
+      out[w] = word;
+    }
+    return;
+  }
+  const int tpr = a.d / 8;
+  const int slots = g.nblk * g.block;
+  const long long at = static_cast<long long>(blockIdx.x - a.mask_ctas) * (kPrepThreads / tpr) + threadIdx.x / tpr;
+  const int c = threadIdx.x % tpr;
+  const bool in = at < static_cast<long long>(a.BH) * slots;
+  const int bh = in ? static_cast<int>(at / slots) : 0, slot = in ? static_cast<int>(at - static_cast<long long>(bh) * slots) : 0;
+  const int kind = a.kinds[bh];
+  int token = in && kind <= kCube ? token_of_slot(g, kind, slot) : -1;
+  float delta = 0.f, lse = -INFINITY;
+  if (token >= 0) {
+    // whole call: O, dO and LSE in natural order; lists: each head's own layout and set
+    const bool perm = !a.by_token && a.has_perm && kind != kSpatial;
+    const int r = a.by_token ? token : slot;
+    const int stride = a.by_token ? g.N : (perm ? g.R : a.nat_rows);
+    const size_t rowi = static_cast<size_t>(bh) * stride + r;
+    const void* o = perm ? a.o_perm : a.o_nat;
+    const void* go = perm ? a.do_perm : a.do_nat;
+    const float* dl = perm ? a.dlse_perm : a.dlse_nat;
+    delta = dot8(load8(o, rowi * a.d + c * 8, a.f32), load8(go, rowi * a.d + c * 8, a.f32));
+    lse = (perm ? a.lse_perm : a.lse_nat)[rowi];
+    if (c == 0 && dl != nullptr) delta -= dl[rowi];
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1)
+    if (off < tpr) delta += __shfl_xor_sync(0xffffffffu, delta, off);
+  if (in && c == 0) {
+    const bool sees = lse != -INFINITY;
+    float* t = a.terms + (static_cast<size_t>(bh) * g.nblk + slot / g.block) * (2 * g.block) + slot % g.block;
+    t[0] = sees ? -lse * 1.4426950408889634f : -INFINITY;
+    t[g.block] = sees ? -delta : 0.f;
+  }
+}
+
+template <int D, int BN>
+cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, const BwdArgs& a, cudaStream_t stream) {
+  auto kern = sparse_attn_bwd_kernel<D, BN>;
+  const int smem = BwdCfg<D, BN>::smem_bytes((a.g.nblk + 31) / 32);
+  if (smem > 232448) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(2 * a.BH * a.g.nblk), kBwdThreads, smem, stream>>>(nat, perm, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool sparse_attn_bwd_fits(const Geom& g, int BH) {
+  return BwdCfg<128, 128>::smem_bytes((g.nblk + 31) / 32) <= 232448 &&
+         2LL * BH * g.nblk <= 0x7fffffffLL && static_cast<long long>(BH) * g.nblk * g.block / 8 <= 0x7fffffffLL;
+}
+
+cudaError_t launch_sparse_attn_bwd(const BwdMaps& nat, const BwdMaps& perm, BwdPrep prep, const BwdArgs& a, int d,
+                                   cudaStream_t stream) {
+  const long long lists = static_cast<long long>(a.BH) * a.g.nblk;
+  const long long slots = lists * a.g.block;
+  const int rows_per_cta = kPrepThreads / (d / 8);
+  prep.mask_ctas = static_cast<int>((lists + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
+  const long long grid = prep.mask_ctas + (slots + rows_per_cta - 1) / rows_per_cta;
+  bwd_prep_kernel<<<static_cast<unsigned>(grid), kPrepThreads, 0, stream>>>(prep);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int bn = a.g.block;
+  if (d == 128 && bn == 128) return launch_bwd_t<128, 128>(nat, perm, a, stream);
+  if (d == 64 && bn == 128) return launch_bwd_t<64, 128>(nat, perm, a, stream);
+  if (d == 128 && bn == 64) return launch_bwd_t<128, 64>(nat, perm, a, stream);
+  if (d == 64 && bn == 64) return launch_bwd_t<64, 64>(nat, perm, a, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace vsa

@@ -84,6 +84,44 @@ struct AttnArgs {
 cudaError_t launch_sparse_attn(const AttnMaps& nat, const AttnMaps& perm, const AttnArgs& a, int d,
                                cudaStream_t stream);
 
+// Gradient of the attention (see attn_bwd.cu): tensor maps of one set, the row terms and row
+// bitsets, and the main kernel's arguments.
+struct BwdMaps {
+  CUtensorMap q, k, v, g, dq, dk, dv;  // g: dO
+};
+
+struct BwdPrep {
+  const uint8_t* kinds;
+  const int32_t* kv_idx;
+  const int32_t* kv_cnt;
+  const void *o_nat, *o_perm, *do_nat, *do_perm;
+  const float *lse_nat, *lse_perm, *dlse_nat, *dlse_perm;
+  uint32_t* rbits;  // [BH, nblk, ceil(nblk / 32)] kept key blocks of every query block
+  float* terms;     // [BH, nblk, 2, block]: -lse * log2 e (-inf: the row sees nothing), then -delta
+  int* err;
+  int BH, d, max_kv, has_perm, nat_rows;
+  int by_token;     // O, dO and LSE are in natural order for every head (the whole call)
+  int f32;          // O and dO are fp32 rows
+  int mask_ctas;    // set by the launcher
+  Geom g;
+};
+
+struct BwdArgs {
+  const uint8_t* kinds;
+  const uint32_t* rbits;
+  const float* terms;
+  int* err;
+  void *nat_dq, *nat_dk, *nat_dv;  // zeroed for a head with an invalid kind byte
+  int BH, has_perm, nat_rows;
+  float scale, scale_log2;
+  Geom g;
+};
+
+// Whether the shape's bitsets fit the kernel's shared memory and its grid.
+bool sparse_attn_bwd_fits(const Geom& g, int BH);
+cudaError_t launch_sparse_attn_bwd(const BwdMaps& nat, const BwdMaps& perm, BwdPrep prep, const BwdArgs& a, int d,
+                                   cudaStream_t stream);
+
 // Profiling (see profile.cu).
 struct ProfilePlan {
   int r;        // sampled rows

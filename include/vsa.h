@@ -378,6 +378,63 @@ VSA_API vsa_status vsa_attention_workspace_layout(const vsa_shape *shape, const 
                                           size_t *off_kv_cnt, int *max_kv);
 
 /* ---------------------------------------------------------------------------------------
+ * Gradients.  The pages have no counterpart (they train nothing here); the formulas are the
+ * derivative of the attention the forward calls compute, with the masks taken as constants.
+ * ------------------------------------------------------------------------------------- */
+
+/* Pointers of one gradient problem, all [B, H, rows, d] or [B, H, rows]; dq, dk and dv are
+ * written and overlap no input.  d_lse (the gradient of the log-sum-exp) may be NULL. */
+typedef struct {
+    const void *q, *k, *v, *o;    /* the forward call's inputs and output */
+    const void *d_o;              /* gradient of o */
+    const float *lse;             /* the forward call's log-sum-exp (required) */
+    const float *d_lse;           /* gradient of lse, or NULL */
+    void *dq, *dk, *dv;
+} vsa_qkvo_grad;
+
+/* Workspace bytes of vsa_sparse_attn_bwd: a bitset of the lists (B*H*nblk*ceil(nblk/32) words)
+ * and two fp32 terms per row; 0 for a shape that is invalid or too large. */
+VSA_API size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape *shape);
+
+/*
+ * Gradient of vsa_sparse_attn_fwd: with P = exp(scale q k^T - lse) on the kept block pairs and
+ * delta = rowsum(d_o * o) - d_lse,
+ *   dv = P^T d_o,   dS = P * (d_o v^T - delta),   dq = scale dS k,   dk = scale dS^T q.
+ * P and dS are rounded to bf16 in front of their tensor products, every sum is fp32, the
+ * gradients are bf16.  Each is written by one owner: two runs give the same bits.
+ *   natural, permuted   as for vsa_sparse_attn_fwd (permuted may be NULL); bf16; padding slots
+ *                       of cube layouts hold finite values, zero as vsa_permute leaves them.
+ *                       Every row of a head's layout is written, rows that hold no token or
+ *                       that nothing sees with zeros
+ *   d_kind, d_kv_idx, d_kv_cnt, max_kv, scale   the forward call's.  A malformed list sets
+ *                       VSA_DEVERR_KV_RANGE and counts as empty, as in the forward call; a bad
+ *                       kind byte sets VSA_DEVERR_KIND and that head's natural-order gradients
+ *                       are zeros.  A row whose lse is -inf (it sees no key) contributes nothing
+ *   ws                  vsa_sparse_attn_bwd_workspace_size bytes of scratch, one call at a time
+ */
+VSA_API vsa_status vsa_sparse_attn_bwd(const vsa_qkvo_grad *natural, const vsa_qkvo_grad *permuted,
+                                       const uint8_t *d_kind, const int32_t *d_kv_idx, const int32_t *d_kv_cnt,
+                                       int max_kv, const vsa_shape *shape, float scale, void *ws, size_t ws_bytes,
+                                       int *d_err, cudaStream_t stream);
+
+/* Workspace bytes of vsa_attention_bwd (0 for invalid arguments or qk_fp8). */
+VSA_API size_t vsa_attention_bwd_workspace_size(const vsa_shape *shape, const vsa_params *params, vsa_dtype dtype);
+
+/*
+ * Gradient of vsa_attention: permute -> masks -> vsa_sparse_attn_bwd -> unpermute, on `stream`.
+ * The masks are built again from the kinds (and, for cube heads, from q and k), so nothing of
+ * the forward call's workspace is needed.
+ *   io       natural q, k, v, o, d_o, lse (d_lse or NULL); dq, dk, dv written; rows in dtype
+ *   d_kind   [B*H] the kinds the forward call used (given, or as it wrote them)
+ *   params   the forward call's; layout_in_kernel is accepted and changes nothing here, qk_fp8
+ *            returns VSA_ERR_UNSUPPORTED (the e4m3 codes have no gradient)
+ *   ws       vsa_attention_bwd_workspace_size bytes, one call at a time
+ */
+VSA_API vsa_status vsa_attention_bwd(const vsa_qkvo_grad *io, vsa_dtype dtype, const vsa_shape *shape,
+                                     const vsa_params *params, const uint8_t *d_kind, void *ws, size_t ws_bytes,
+                                     int *d_err, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Semantic-aware permutation ("Sparse VideoGen2" page, abstract: tokens clustered by
  * k-means and reordered by cluster, a top-p budget over clusters).  The page gives no
  * formulas; the readings:
