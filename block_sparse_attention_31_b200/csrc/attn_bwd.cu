@@ -44,54 +44,60 @@ namespace vsa {
 namespace {
 
 constexpr int kBwdThreads = 384;
-constexpr int kWarpX = 8, kWarpMma = 9, kWarpY = 10;
+constexpr int kWarpX = 8, kWarpMma = 9, kWarpY = 10, kWarpT = 11;
 constexpr int kBM = 128;
+constexpr int kMaxSmem = 232448;
 constexpr int kRegsSoftmax = 208, kRegsCtl = 88;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl == 384 * 168, "register split must equal the launch total");
-constexpr int kPolyPairs8 = 1;  // probability pairs in 8 whose exponentials run on the FMA pipe
 
-template <int D, int BN>
+template <int D, int BN, bool kKey>
 struct BwdCfg {
-  static constexpr int NX = D * BN == 128 * 128 ? 3 : 4;  // ring stages of X (Q or K)
-  static constexpr int NY = D * BN == 128 * 128 ? 1 : 2;  // ring stages of Y (dO or V)
+  // Ring stages of X (Q or K) and Y (dO or V).  A tile takes about 1500 cycles to arrive; with a spare
+  // stage of each no product waits for it.  The
+  // spare X stage is given up where the bitset of a very long head needs its place.
+  [[maybe_unused]] static constexpr int NX_MOST = 3, NX_LEAST = 2, NY = 2, NT = 2;
   static constexpr int A_BYTES = kBM * D * 2;             // a resident tile (M = 128 lanes, BN rows loaded)
   static constexpr int T_BYTES = BN * D * 2;              // a ring tile
   static constexpr int ST_BYTES = 2 * BN * 4;             // the rows' two terms of a block
   static constexpr int PANELS = D / 64;
   static constexpr int OFF_A0 = 0;                        // K (key CTA) or Q (query CTA)
   static constexpr int OFF_A1 = OFF_A0 + A_BYTES;         // V or dO
-  static constexpr int OFF_X = OFF_A1 + A_BYTES;
-  static constexpr int OFF_Y = OFF_X + NX * T_BYTES;
-  static constexpr int OFF_ST = OFF_Y + NY * T_BYTES;
-  static constexpr int OFF_BAR = OFF_ST + NX * ST_BYTES;
-  static constexpr int NBAR = 32;
+  // X is the last ring, behind it the small things: its number of stages moves only those.
+  static constexpr int OFF_Y = OFF_A1 + A_BYTES;
+  static constexpr int OFF_X = OFF_Y + NY * T_BYTES;
+  static constexpr int NBAR = 28;
+  // behind the nx stages of X: the rows' terms of NT blocks, barriers, TMEM base and abort flag, bitset
+  static constexpr int OFF_BAR = NT * ST_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_BITS = OFF_MISC + 64;
-  // TMEM columns.  Key CTA: S, dP, dV, dK.  Query CTA: S of two blocks, dP, dQ.
-  static constexpr int TM_S = 0;
-  static constexpr int TM_DP_K = BN, TM_DV = 2 * BN, TM_DK = 2 * BN + D;
-  static constexpr int TM_DP_Q = 2 * BN, TM_DQ = 3 * BN;
-  static constexpr int TM_USED = (2 * BN + 2 * D) > (3 * BN + D) ? (2 * BN + 2 * D) : (3 * BN + D);
-  static constexpr int TM_COLS = TM_USED <= 256 ? 256 : 512;
+  static constexpr int OFF_BITS = OFF_MISC + 16;
+  // TMEM columns.  S; dP with P and dS (packed bf16) written over it once it has been read: each half
+  // of the columns holds its threads' dP, then P (key CTA only) and dS.  Behind them dV and dK, or dQ
+  // and the query block's Q and dO as A operands.
+  static constexpr int TM_S = 0, TM_DP = BN, TM_DS = kKey ? BN / 4 : 0, TM_ACC = 2 * BN;
+  static constexpr int TM_Q = TM_ACC + D, TM_DO = TM_Q + D / 2;
+  static constexpr int TM_COLS = 2 * BN + 2 * D <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(kBM, BN, false, false);
   static constexpr uint32_t IDESC_G = idesc_bf16_f32(kBM, D, false, true);
-  static int smem_bytes(int nwords) { return OFF_BITS + 4 * nwords + 1024; }
+  static int smem_bytes(int nx, int nwords) { return OFF_X + nx * T_BYTES + OFF_BITS + 4 * nwords; }
+  static int stages(int nwords) { return smem_bytes(NX_MOST, nwords) <= kMaxSmem ? NX_MOST : NX_LEAST; }
 };
 
 enum {
   B_A0 = 0,
   B_A1 = 1,
-  B_FULL_X = 2,    // +stage (up to 4)
-  B_REL_X = 6,     // +stage
-  B_FULL_Y = 10,   // +stage (up to 4)
-  B_REL_Y = 14,    // +stage
-  B_FULL_ST = 18,  // +stage of X
-  B_S = 22,        // +buffer
-  B_DP = 24,
-  B_P = 25,
-  B_DS = 26,
-  B_FINAL = 27,
+  B_FULL_X = 2,    // +stage
+  B_REL_X = 5,     // +stage
+  B_FULL_Y = 8,    // +stage
+  B_REL_Y = 10,    // +stage
+  B_FULL_T = 12,   // +stage of the rows' terms
+  B_S = 14,        // S (dP) is in TMEM
+  B_DP = 15,
+  B_SREAD = 16,    // S has been read into registers
+  B_P = 17,        // key CTA: P is written; query CTA, once: Q and dO are in TMEM
+  B_DS = 18,       // dS is written
+  B_FINAL = 19,
 };
+constexpr int kSoftmaxWarps = 8;  // arrivals on B_SREAD, B_P and B_DS: one per warp
 
 // The set bits of a bitset in ascending order.
 struct BitWalk {
@@ -107,9 +113,9 @@ struct BitWalk {
   }
 };
 
-// p = 2^x of a packed pair; pair c of a row's half.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int c) {
-  if ((c & 7) >= 8 - kPolyPairs8) return exp2_poly2(x);
+// 2^x of a packed pair.  All on the hardware exponential: moving one pair in 8 (2, 3) to the FMA pipe, as
+// the forward kernel does, measured 0.7% (1.2%, 1.7%) slower on 12 x 32760 rows.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
   float x0, x1;
   f2_split(x, x0, x1);
   return f2_make(fast_exp2(x0), fast_exp2(x1));
@@ -159,16 +165,16 @@ __device__ __forceinline__ void stage_rows(uint8_t* stage, uint32_t taddr, int c
 // kKey: a key CTA (dK, dV of block `blk`); else a query CTA (dQ of block `blk`).
 template <int D, int BN, bool kKey>
 __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, const BwdArgs& a, int bh, int blk,
-                                        uint8_t* smem_raw) {
-  using C = BwdCfg<D, BN>;
+                                        uint8_t* smem) {
+  using C = BwdCfg<D, BN, kKey>;
   constexpr int H = BN / 2;  // columns per thread
-  const uint32_t raw_u32 = smem_u32(smem_raw);
-  const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (sbase - raw_u32);
-  auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * i; };
-  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);  // [0] TMEM base, [1] abort flag
+  const uint32_t sbase = smem_u32(smem);
+  const int nx = a.nx;
+  const uint32_t rest = C::OFF_X + nx * C::T_BYTES;
+  auto bar = [&](int i) -> uint32_t { return sbase + rest + C::OFF_BAR + 8u * i; };
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + rest + C::OFF_MISC);  // [0] TMEM base, [1] abort flag
   volatile int* abort_flag = misc + 1;
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + rest + C::OFF_BITS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Geom& g = a.g;
   const int nwords = (g.nblk + 31) >> 5;
@@ -194,50 +200,65 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
   if (blk >= nb_head) return;
   const BwdMaps* m = a.has_perm && kind != kSpatial ? mp : mn;
 
-  // ---- the blocks this CTA walks, barriers, TMEM ----
-  const uint32_t* rbits = a.rbits + static_cast<size_t>(bh) * g.nblk * nwords;
-  if (kKey) {
-    for (int w = warp; w < nwords; w += kBwdThreads / 32) {
-      const int r = w * 32 + lane;
-      const bool keeps = r < nb_head && ((rbits[static_cast<size_t>(r) * nwords + (blk >> 5)] >> (blk & 31)) & 1u);
-      const uint32_t word = __ballot_sync(0xffffffffu, keeps);
-      if (lane == 0) bits[w] = word;
-    }
-  } else {
-    for (int w = tid; w < nwords; w += kBwdThreads) bits[w] = rbits[static_cast<size_t>(blk) * nwords + w];
-  }
+  // ---- barriers, the resident tiles, the blocks this CTA walks, TMEM ----
   bool stop = false;
-  if (tid == 0) {
+  if (tid == kWarpX * 32) {
     stop = (*reinterpret_cast<volatile int*>(a.err) & kDevErrTimeout) != 0;
     mbar_init(bar(B_A0), 1);
     mbar_init(bar(B_A1), 1);
-    for (int s = 0; s < C::NX; ++s) {
+    for (int s = 0; s < C::NX_MOST; ++s) {
       mbar_init(bar(B_FULL_X + s), 1);
       mbar_init(bar(B_REL_X + s), 1);
-      mbar_init(bar(B_FULL_ST + s), 1);
     }
     for (int s = 0; s < C::NY; ++s) {
       mbar_init(bar(B_FULL_Y + s), 1);
       mbar_init(bar(B_REL_Y + s), 1);
     }
+    for (int s = 0; s < C::NT; ++s) mbar_init(bar(B_FULL_T + s), 1);
     mbar_init(bar(B_S), 1);
-    mbar_init(bar(B_S + 1), 1);
     mbar_init(bar(B_DP), 1);
-    mbar_init(bar(B_P), 256);
-    mbar_init(bar(B_DS), 256);
+    mbar_init(bar(B_SREAD), kSoftmaxWarps);
+    mbar_init(bar(B_P), kSoftmaxWarps);
+    mbar_init(bar(B_DS), kSoftmaxWarps);
     mbar_init(bar(B_FINAL), 1);
     misc[1] = 0;
     mbar_init_fence();
+    if (!stop) {  // K and V, or Q and dO, land while the list is built
+      mbar_arrive_expect_tx(bar(B_A0), C::T_BYTES);
+      mbar_arrive_expect_tx(bar(B_A1), C::T_BYTES);
+#pragma unroll
+      for (int c = 0; c < C::PANELS; ++c) {
+        tma_load_3d(sbase + C::OFF_A0 + c * kBM * 128, kKey ? &m->k : &m->q, bar(B_A0), c * 64, blk * BN, bh);
+        tma_load_3d(sbase + C::OFF_A1 + c * kBM * 128, kKey ? &m->v : &m->g, bar(B_A1), c * 64, blk * BN, bh);
+      }
+      tma_prefetch_desc(kKey ? &m->q : &m->k);
+      tma_prefetch_desc(kKey ? &m->g : &m->v);
+    }
   }
-  if (__syncthreads_or(stop)) return;
   if (warp == kWarpMma) {
-    tmem_alloc(sbase + C::OFF_MISC, C::TM_COLS);
+    tmem_alloc(sbase + rest + C::OFF_MISC, C::TM_COLS);
     tmem_relinquish();
   }
+  const uint32_t* rbits = a.rbits + static_cast<size_t>(bh) * g.nblk * nwords;
+  if (kKey) {
+    for (int w = warp; w < nwords; w += kSoftmaxWarps) {
+      if (warp >= kSoftmaxWarps) break;
+      const int r = w * 32 + lane;
+      const bool keeps = r < nb_head && ((rbits[static_cast<size_t>(r) * nwords + (blk >> 5)] >> (blk & 31)) & 1u);
+      const uint32_t word = __ballot_sync(0xffffffffu, keeps);
+      if (lane == 0) bits[w] = word;
+    }
+  } else if (warp < kSoftmaxWarps) {
+    for (int w = tid; w < nwords; w += kSoftmaxWarps * 32) bits[w] = rbits[static_cast<size_t>(blk) * nwords + w];
+  }
   tc_fence_before();
-  __syncthreads();
+  stop = __syncthreads_or(stop);
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  if (stop) {  // another CTA gave up waiting: nothing is in flight here
+    if (warp == kWarpMma) tmem_dealloc(tmem, C::TM_COLS);
+    return;
+  }
   int U = 0;
   for (int w = lane; w < nwords; w += 32) U += __popc(bits[w]);
 #pragma unroll
@@ -245,19 +266,13 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsCtl>();
+    const bool one = elect_one();
     if (warp == kWarpX || warp == kWarpY) {
       // ================= TMA producers =================
-      if (lane == 0 && U > 0) {
+      if (one) {
         const bool isx = warp == kWarpX;
-        // resident tile
-        const CUtensorMap* ta = kKey ? (isx ? &m->k : &m->v) : (isx ? &m->q : &m->g);
-        const uint32_t dst_a = sbase + (isx ? C::OFF_A0 : C::OFF_A1), bar_a = bar(isx ? B_A0 : B_A1);
-        mbar_arrive_expect_tx(bar_a, C::T_BYTES);
-#pragma unroll
-        for (int c = 0; c < C::PANELS; ++c) tma_load_3d(dst_a + c * kBM * 128, ta, bar_a, c * 64, blk * BN, bh);
-        // ring
         const CUtensorMap* tr = kKey ? (isx ? &m->q : &m->g) : (isx ? &m->k : &m->v);
-        const int ns = isx ? C::NX : C::NY;
+        const int ns = isx ? nx : C::NY;
         const int full0 = isx ? B_FULL_X : B_FULL_Y, rel0 = isx ? B_REL_X : B_REL_Y;
         const uint32_t dst_r = sbase + (isx ? C::OFF_X : C::OFF_Y);
         BitWalk walk(bits);
@@ -269,32 +284,51 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
 #pragma unroll
           for (int c = 0; c < C::PANELS; ++c)
             tma_load_3d(dst_r + st * C::T_BYTES + c * BN * 128, tr, bar(full0 + st), c * 64, b * BN, bh);
-          if (kKey && isx) {
-            mbar_arrive_expect_tx(bar(B_FULL_ST + st), C::ST_BYTES);
-            bulk_load(sbase + C::OFF_ST + st * C::ST_BYTES,
-                      a.terms + (static_cast<size_t>(bh) * g.nblk + b) * (2 * BN), C::ST_BYTES, bar(B_FULL_ST + st));
-          }
           issued = n + 1;
           if (++st == ns) {
             st = 0;
             ph ^= 1;
           }
         }
-        if (*abort_flag) {  // every copy this thread issued lands before the CTA exits
-          mbar_wait_drain(bar_a, 0, a.err);
+        // every copy lands before the CTA exits; without an abort the products have waited for all but
+        // the resident tiles of an empty list
+        if (*abort_flag || U == 0) {
+          mbar_wait_drain(bar(isx ? B_A0 : B_A1), 0, a.err);
           for (int s = 0; s < ns; ++s) {
             int last = -1;
             for (int n = s; n < issued; n += ns) last = n;
-            if (last < 0) continue;
-            mbar_wait_drain(bar(full0 + s), (last / ns) & 1, a.err);
-            if (kKey && isx) mbar_wait_drain(bar(B_FULL_ST + s), (last / ns) & 1, a.err);
+            if (last >= 0) mbar_wait_drain(bar(full0 + s), (last / ns) & 1, a.err);
           }
         }
       }
       __syncwarp();
+    } else if (kKey && warp == kWarpT) {
+      // ================= the rows' terms, two blocks ahead =================
+      if (one && U > 0) {
+        BitWalk walk(bits);
+        int rs = 0, rp = 0, issued = 0;  // X stage and parity of the release two blocks back
+        for (int n = 0; n < U; ++n) {
+          const int b = walk.next(), st = n % C::NT;
+          if (n >= C::NT) {  // block n - NT's dS is written once its dK product has been issued
+            if (!mbar_wait(bar(B_REL_X + rs), rp, abort_flag, a.err)) break;
+            if (++rs == nx) {
+              rs = 0;
+              rp ^= 1;
+            }
+          }
+          mbar_arrive_expect_tx(bar(B_FULL_T + st), C::ST_BYTES);
+          bulk_load(sbase + rest + st * C::ST_BYTES, a.terms + (static_cast<size_t>(bh) * g.nblk + b) * (2 * BN),
+                    C::ST_BYTES, bar(B_FULL_T + st));
+          issued = n + 1;
+        }
+        if (*abort_flag)
+          for (int n = max(0, issued - C::NT); n < issued; ++n)
+            mbar_wait_drain(bar(B_FULL_T + n % C::NT), (n / C::NT) & 1, a.err);
+      }
+      __syncwarp();
     } else if (warp == kWarpMma) {
       // ================= tcgen05 issuer =================
-      if (lane == 0 && U > 0) {
+      if (one && U > 0) {
         const uint64_t da0 = sdesc_sw128(sbase + C::OFF_A0, 16, 1024), da1 = sdesc_sw128(sbase + C::OFF_A1, 16, 1024);
         // ring tiles as K-major (S, dP) and MN-major (gradient) B operands
         const uint64_t dxk = sdesc_sw128(sbase + C::OFF_X, 16, 1024);
@@ -305,20 +339,26 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
         bool ok = true;
         int xs = 0, xp = 0, ys = 0, yp = 0;  // next X and Y stage to be read by S and dP
         int xr = 0, yr = 0;                  // stage of the gradient product
+        int ts = 0, tp = 0;                  // stage of the rows' terms
+        static_assert(C::NT == 2, "ts alternates");
         auto wait = [&](int b, int parity) {
           if (ok && !mbar_wait(bar(b), parity, abort_flag, a.err)) ok = false;
           return ok;
         };
-        // D[lanes, BN] = A (resident) * ring tile^T
-        auto product = [&](uint32_t d_tm, uint64_t da, uint64_t db) {
+        // D[lanes, BN] = A * ring tile^T, A from shared memory (key CTA) or TMEM (query CTA)
+        auto product = [&](uint32_t d_tm, uint64_t a_sm, uint32_t a_tm, uint64_t db) {
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ss(d_tm, da + static_cast<uint64_t>(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) / 16),
-                      db + static_cast<uint64_t>(((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16), C::IDESC_S,
-                      kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b = db + static_cast<uint64_t>(((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16);
+            if constexpr (kKey)
+              tc_mma_ss(d_tm, a_sm + static_cast<uint64_t>(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) / 16), b,
+                        C::IDESC_S, kk > 0 ? 1u : 0u);
+            else
+              tc_mma_ts(d_tm, a_tm + kk * 8, b, C::IDESC_S, kk > 0 ? 1u : 0u);
+          }
         };
-        // acc[lanes, D] += packed bf16 (TMEM, two halves of the columns) * ring tile
+        // acc[lanes, D] += packed bf16 (TMEM, two halves) * ring tile
         auto accumulate = [&](uint32_t d_tm, uint32_t a_tm, uint64_t db, bool first) {
           tc_fence_after();
 #pragma unroll
@@ -326,18 +366,24 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
             tc_mma_ts(d_tm, a_tm + (kk < BN / 32 ? kk * 8 : H + (kk - BN / 32) * 8),
                       db + static_cast<uint64_t>(kk * 16 * 128 / 16), C::IDESC_G, first && kk == 0 ? 0u : 1u);
         };
-        auto next_s = [&](int buf) {
+        auto next_s = [&](bool first, int parity) {
           if (!wait(B_FULL_X + xs, xp)) return;
-          product(tmem + C::TM_S + buf * BN, da0, dxk + xs * kStage);
-          tc_commit(bar(B_S + buf));
-          if (++xs == C::NX) {
+          if (kKey) {  // the threads' terms of the block: S says that they are there
+            if (!wait(B_FULL_T + ts, tp)) return;
+            ts ^= 1;
+            tp ^= ts == 0;
+          }
+          if (!first && !wait(B_SREAD, parity)) return;
+          product(tmem + C::TM_S, da0, tmem + C::TM_Q, dxk + xs * kStage);
+          tc_commit(bar(B_S));
+          if (++xs == nx) {
             xs = 0;
             xp ^= 1;
           }
         };
         auto next_dp = [&]() {
           if (!wait(B_FULL_Y + ys, yp)) return;
-          product(tmem + (kKey ? C::TM_DP_K : C::TM_DP_Q), da1, dyk + ys * kStage);
+          product(tmem + C::TM_DP, da1, tmem + C::TM_DO, dyk + ys * kStage);
           tc_commit(bar(B_DP));
           if (!kKey) tc_commit(bar(B_REL_Y + ys));
           if (++ys == C::NY) {
@@ -345,34 +391,30 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
             yp ^= 1;
           }
         };
-        wait(B_A0, 0);
-        if (ok) next_s(0);
-        if (ok) wait(B_A1, 0);
+        // S of the next block is issued as soon as S has been read, and runs under the exponentials.
+        // Products of one thread complete in order, so B_DP of a block says that the products of the
+        // block before have read P and dS, which then may be written over dP.
+        if (kKey) {
+          wait(B_A0, 0);
+          wait(B_A1, 0);
+        } else {
+          wait(B_P, 0);
+        }
+        if (ok) next_s(true, 0);
         if (ok) next_dp();
-        if constexpr (kKey) {
-          for (int n = 0; ok && n < U; ++n) {
+        for (int n = 0; ok && n < U; ++n) {
+          if (n + 1 < U) next_s(false, n & 1);
+          if constexpr (kKey) {
             if (!wait(B_P, n & 1)) break;
-            accumulate(tmem + C::TM_DV, tmem + C::TM_S, dym + yr * kStage, n == 0);
+            accumulate(tmem + C::TM_ACC, tmem + C::TM_DP, dym + yr * kStage, n == 0);
             tc_commit(bar(B_REL_Y + yr));
             if (++yr == C::NY) yr = 0;
-            if (n + 1 < U) next_s(0);
-            if (!wait(B_DS, n & 1)) break;
-            accumulate(tmem + C::TM_DK, tmem + C::TM_DP_K, dxm + xr * kStage, n == 0);
-            tc_commit(bar(B_REL_X + xr));
-            if (++xr == C::NX) xr = 0;
-            if (n + 1 < U) next_dp();
           }
-        } else {
-          if (ok && U > 1) next_s(1);
-          for (int n = 0; ok && n < U; ++n) {
-            if (!wait(B_DS, n & 1)) break;
-            if (n + 1 < U) next_dp();
-            if (!ok) break;
-            accumulate(tmem + C::TM_DQ, tmem + C::TM_S + (n & 1) * BN, dxm + xr * kStage, n == 0);
-            tc_commit(bar(B_REL_X + xr));
-            if (++xr == C::NX) xr = 0;
-            if (n + 2 < U) next_s(n & 1);
-          }
+          if (!wait(B_DS, n & 1)) break;
+          accumulate(tmem + C::TM_ACC + (kKey ? D : 0), tmem + C::TM_DP + C::TM_DS, dxm + xr * kStage, n == 0);
+          tc_commit(bar(B_REL_X + xr));
+          if (++xr == nx) xr = 0;
+          if (n + 1 < U) next_dp();
         }
         // all MMAs of this thread complete before the accumulators are read or TMEM is released
         tc_commit(bar(B_FINAL));
@@ -395,23 +437,51 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
       nl_row = f2_make(nl, nl);
       nd_row = f2_make(nd, nd);
     }
+    const uint32_t t_s = t_lane + C::TM_S + half * H, t_dp = t_lane + C::TM_DP + half * H;
     bool ok = true;
+    auto wait = [&](int b, int parity) {
+      ok = mbar_wait(bar(b), parity, abort_flag, a.err) && ok;
+      __syncwarp();
+    };
+    auto arrive = [&](int b) {  // this warp's TMEM loads or stores are done
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    if (!kKey && U > 0) {
+      // Q (warps 0-3) and dO (4-7) into TMEM, packed as they are: as A operands read from there they leave
+      // the shared memory's bandwidth to the ring tiles
+      wait(half ? B_A1 : B_A0, 0);
+      const uint8_t* tile = smem + (half ? C::OFF_A1 : C::OFF_A0);
+#pragma unroll
+      for (int c = 0; c < C::PANELS; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(r + ch * 4) =
+              *reinterpret_cast<const uint4*>(tile + c * (kBM * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+        tmem_st_cols<32>(t_lane + (half ? C::TM_DO : C::TM_Q) + c * 32, r);
+      }
+      arrive(B_P);
+    }
     BitWalk walk(bits);
-    int st = 0, ph = 0;
+    // A wait costs 100 to 200 cycles even when its barrier has completed (the tensor core keeps the
+    // shared memory busy), so the barriers are tested ahead, under arithmetic.
+    bool s_in = false, dp_in = false;
     for (int n = 0; n < U; ++n) {
       const int b = walk.next();
-      const int buf = kKey ? 0 : (n & 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + buf), kKey ? (n & 1) : ((n >> 1) & 1), abort_flag, a.err));
-      if (ok && kKey) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FULL_ST + st), ph, abort_flag, a.err));
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;  // after a wait that gave up the rest runs on without waiting
+      // (the issuer waits for the block's terms before it issues S)
+      if (!__all_sync(0xffffffffu, s_in)) wait(B_S, n & 1);
       tc_fence_after();
-      const uint32_t t_s = t_lane + C::TM_S + buf * BN + half * H;
-      const uint32_t t_dp = t_lane + (kKey ? C::TM_DP_K : C::TM_DP_Q) + half * H;
-      const uint64_t* terms = reinterpret_cast<const uint64_t*>(smem + C::OFF_ST + st * C::ST_BYTES) + half * (H / 2);
+      // -lse * log2 e and, BN floats on, -delta of this thread's columns: the same address for a warp
+      const ulonglong2* terms =
+          reinterpret_cast<const ulonglong2*>(smem + rest + (n % C::NT) * C::ST_BYTES) + half * (H / 4);
       uint64_t p[H / 2];
       {
         uint32_t r[H];
         tmem_ld_cols<H>(t_s, r);
+        arrive(B_SREAD);
         if (!kKey && !block_full(g, kind, b)) {  // key columns that hold no token (ragged tail, cube padding)
 #pragma unroll
           for (int w = 0; w < H / 32; ++w) {
@@ -422,49 +492,53 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
           }
         }
 #pragma unroll
-        for (int c = 0; c < H / 2; ++c)
-          p[c] = exp2_pair(f2_fma(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sl2,
-                                  kKey ? terms[c] : nl_row),
-                           c);
+        for (int c = 0; c < H / 2; c += 2) {
+          if (c == H / 8 * 3) dp_in = mbar_test(bar(B_DP), n & 1);
+          const ulonglong2 nl = kKey ? terms[c / 2] : make_ulonglong2(nl_row, nl_row);
+          p[c] = exp2_pair(f2_fma(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), sl2, nl.x));
+          p[c + 1] =
+              exp2_pair(f2_fma(f2_make(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3])), sl2, nl.y));
+        }
       }
+      if (!__all_sync(0xffffffffu, dp_in)) wait(B_DP, n & 1);
+      tc_fence_after();
+      uint32_t r[H];
+      tmem_ld_cols<H>(t_dp, r);
       if constexpr (kKey) {
         uint32_t pk[H / 2];
 #pragma unroll
         for (int c = 0; c < H / 2; ++c) pk[c] = pack_pair(p[c]);
-        tmem_st_cols<H / 2>(t_s, pk);
-        tc_fence_before();
-        mbar_arrive(bar(B_P));
+        tmem_st_cols<H / 2>(t_dp, pk);
+        arrive(B_P);
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(B_DP), n & 1, abort_flag, a.err));
-      if (!ok) break;
-      tc_fence_after();
-      {
-        uint32_t r[H];
-        tmem_ld_cols<H>(t_dp, r);
-        uint32_t pk[H / 2];
+      s_in = n + 1 < U && mbar_test(bar(B_S), (n + 1) & 1);
+      uint32_t pk[H / 2];
 #pragma unroll
-        for (int c = 0; c < H / 2; ++c)
-          pk[c] = pack_pair(f2_mul(p[c], f2_add(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])),
-                                                kKey ? terms[BN / 2 + c] : nd_row)));
-        tmem_st_cols<H / 2>(kKey ? t_dp : t_s, pk);
+      for (int c = 0; c < H / 2; c += 2) {
+        const ulonglong2 nd = kKey ? terms[BN / 4 + c / 2] : make_ulonglong2(nd_row, nd_row);
+        pk[c] =
+            pack_pair(f2_mul(p[c], f2_add(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), nd.x)));
+        pk[c + 1] = pack_pair(
+            f2_mul(p[c + 1], f2_add(f2_make(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3])), nd.y)));
       }
-      tc_fence_before();
-      mbar_arrive(bar(B_DS));
-      if (++st == C::NX) {
-        st = 0;
-        ph ^= 1;
-      }
+      tmem_st_cols<H / 2>(t_dp + (kKey ? H / 2 : 0), pk);
+      arrive(B_DS);
     }
+    ok = __all_sync(0xffffffffu, ok);
     // ---- epilogue: accumulators -> bf16 -> swizzled shared memory (over the resident tiles) -> TMA store ----
     if (ok && U > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(B_FINAL), 0, abort_flag, a.err));
       tc_fence_after();
     }
+    if (U == 0) {  // the staging below reuses tiles that nothing has waited for
+      wait(B_A0, 0);
+      wait(B_A1, 0);
+    }
     const bool have = ok && U > 0;
     if constexpr (kKey) {
       // warps 0-3 write dV over V's tile, warps 4-7 dK over K's
       const int off = half ? C::OFF_A0 : C::OFF_A1;
-      stage_rows<BN, D>(smem + off, t_lane + (half ? C::TM_DK : C::TM_DV), 0, row, live, have, half ? a.scale : 1.f);
+      stage_rows<BN, D>(smem + off, t_lane + C::TM_ACC + half * D, 0, row, live, have, half ? a.scale : 1.f);
       fence_proxy_async_smem();
       named_barrier_sync(1 + half, 128);
       if (quad == 2 && lane == 0) {
@@ -472,10 +546,10 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
         for (int c = 0; c < C::PANELS; ++c)
           tma_store_3d(half ? &m->dk : &m->dv, sbase + off + c * BN * 128, c * 64, blk * BN, bh);
         tma_store_commit();
-        tma_store_wait_all();
+        tma_store_wait_read();
       }
     } else {
-      stage_rows<BN, D / 2>(smem + C::OFF_A0, t_lane + C::TM_DQ + half * (D / 2), half * (D / 2), row, live, have,
+      stage_rows<BN, D / 2>(smem + C::OFF_A0, t_lane + C::TM_ACC + half * (D / 2), half * (D / 2), row, live, have,
                             a.scale);
       fence_proxy_async_smem();
       named_barrier_sync(1, 256);
@@ -484,7 +558,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
         for (int c = 0; c < C::PANELS; ++c)
           tma_store_3d(&m->dq, sbase + C::OFF_A0 + c * BN * 128, c * 64, blk * BN, bh);
         tma_store_commit();
-        tma_store_wait_all();
+        tma_store_wait_read();
       }
     }
   }
@@ -498,13 +572,13 @@ template <int D, int BN>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     sparse_attn_bwd_kernel(const __grid_constant__ BwdMaps mn, const __grid_constant__ BwdMaps mp,
                            const __grid_constant__ BwdArgs a) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int per = a.BH * a.g.nblk;
   const int at = static_cast<int>(blockIdx.x);
   const int i = at < per ? at : at - per;
   const int bh = i / a.g.nblk, blk = i - bh * a.g.nblk;
-  if (at < per) bwd_cta<D, BN, true>(&mn, &mp, a, bh, blk, smem_raw);
-  else bwd_cta<D, BN, false>(&mn, &mp, a, bh, blk, smem_raw);
+  if (at < per) bwd_cta<D, BN, true>(&mn, &mp, a, bh, blk, smem);
+  else bwd_cta<D, BN, false>(&mn, &mp, a, bh, blk, smem);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -604,10 +678,13 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
 }
 
 template <int D, int BN>
-cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, const BwdArgs& a, cudaStream_t stream) {
+cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cudaStream_t stream) {
   auto kern = sparse_attn_bwd_kernel<D, BN>;
-  const int smem = BwdCfg<D, BN>::smem_bytes((a.g.nblk + 31) / 32);
-  if (smem > 232448) return cudaErrorInvalidConfiguration;
+  const int nwords = (a.g.nblk + 31) / 32;
+  using C = BwdCfg<D, BN, true>;  // the two kinds of CTA have one layout of shared memory
+  a.nx = C::stages(nwords);
+  const int smem = C::smem_bytes(a.nx, nwords);
+  if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(2 * a.BH * a.g.nblk), kBwdThreads, smem, stream>>>(nat, perm, a);
@@ -617,7 +694,8 @@ cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, const BwdArgs&
 }  // namespace
 
 bool sparse_attn_bwd_fits(const Geom& g, int BH) {
-  return BwdCfg<128, 128>::smem_bytes((g.nblk + 31) / 32) <= 232448 &&
+  using C = BwdCfg<128, 128, true>;
+  return C::smem_bytes(C::NX_LEAST, (g.nblk + 31) / 32) <= kMaxSmem &&
          2LL * BH * g.nblk <= 0x7fffffffLL && static_cast<long long>(BH) * g.nblk * g.block / 8 <= 0x7fffffffLL;
 }
 

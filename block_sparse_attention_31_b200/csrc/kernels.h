@@ -113,6 +113,7 @@ struct BwdArgs {
   int* err;
   void *nat_dq, *nat_dk, *nat_dv;  // zeroed for a head with an invalid kind byte
   int BH, has_perm, nat_rows;
+  int nx;                          // ring stages, set by the launcher
   float scale, scale_log2;
   Geom g;
 };
