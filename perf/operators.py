@@ -351,7 +351,7 @@ def _own(c, s):
             out["y"] = r.y
         return out
     if c["op"] == "norm_bwd":
-        dx, dw = s["norm"].backward(s["dy"], s["x"], s["rstd"], s["w"], dsum=s["dsum"])
+        dx, dw = s["norm"].backward(s["dy"], s["x"], s["rstd"], s["w"], d_sum=s["dsum"])
         return dict(dx=dx, dw=dw)
     shape = (c["B"], c["H"], c["F"] * c["Hl"] * c["Wl"], c["d"])
     q, k, v, do = (s[x].view(shape) for x in ("q", "k", "v", "do"))
