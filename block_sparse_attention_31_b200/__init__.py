@@ -9,7 +9,7 @@ host batches).
 from __future__ import annotations
 
 import contextlib
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -22,6 +22,7 @@ from ._lib import (VSA_BF16, VSA_CUBE, VSA_F32, VSA_SELECT_CUBE, VSA_SELECT_GIVE
                    vsa_sparse_attn_fwd, vsa_sparse_attn_fwd_natural, vsa_unpermute, SemParams, make_sem_params,
                    vsa_quantize_fp8, vsa_sparse_attn_fwd_fp8qk, QKVOGrad, qkvo_grad, vsa_sparse_attn_bwd,
                    vsa_sparse_attn_bwd_workspace_size, vsa_attention_bwd, vsa_attention_bwd_workspace_size,
+                   NormShape, make_norm_shape, vsa_rms_norm, vsa_rms_norm_bwd, vsa_rms_norm_bwd_workspace_size,
                    vsa_gather_rows, vsa_kmeans, vsa_kmeans_workspace_size, vsa_scatter_rows, vsa_semantic_attention,
                    vsa_semantic_mask, vsa_semantic_mask_workspace_size, vsa_semantic_workspace_size)
 
@@ -353,6 +354,150 @@ class SemanticAttention(_HostPipelined):
         return vsa_get_device_error(self.err)
 
 
+class NormOut(NamedTuple):
+    """What one RMSNorm call computed (None for what it was not asked for)."""
+    y: Optional[torch.Tensor]        # [B, H, N, d] in the rows' dtype
+    sum: Optional[torch.Tensor]      # x + residual, rounded to the dtype
+    codes: Optional[torch.Tensor]    # [B, H, N, d] e4m3 codes (uint8) of y / 2^exps
+    exps: Optional[torch.Tensor]     # [B, H, ceil(N / block)] int32
+    rstd: torch.Tensor               # [B, H, N] fp32
+
+
+class _Normalise(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, norm, x, weight, residual):
+        ctx.set_materialize_grads(False)
+        r = norm(x, weight, residual=residual)
+        ctx.norm, ctx.has = norm, (weight is not None, residual is not None)
+        ctx.save_for_backward(x if residual is None else r.sum, r.rstd, weight)
+        return r.y if residual is None else (r.y, r.sum)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, d_sum=None):
+        _no_capture("normalise")
+        s, rstd, weight = ctx.saved_tensors
+        if dy is None:
+            if d_sum is None:
+                return (None,) * 4
+            dy = torch.zeros_like(d_sum, memory_format=torch.contiguous_format)
+        dx, dw = ctx.norm.backward(dy.contiguous(), s, rstd, weight, d_sum=None if d_sum is None else d_sum.contiguous())
+        need = ctx.needs_input_grad
+        return (None, dx if need[1] else None, dw.to(weight.dtype) if need[2] else None, dx if need[3] else None)
+
+
+class RMSNorm:
+    """Root-mean-square norm of [B, H, N] rows of d elements, as in front of the attention's Q and K (H heads
+    of d = 64 or 128), or of whole hidden rows (H = 1): y = s * rstd * weight, s = x + residual.
+
+    quantize: 0 for y in the rows' dtype; 1 for e4m3 codes with one power-of-two scale per row; 64 or 128 for
+              one per so many consecutive rows of a head (d = 64 or 128), the codes and exponents
+              ``vsa_sparse_attn_fwd_fp8qk`` takes.  ``keep_y`` writes y as well.
+    with_grad: the plan also holds the workspace of the weight's gradient (``backward``, ``normalise``); that
+              workspace serves one call at a time.
+
+    x and the residual are any views whose last dimension is dense, a [B, N, H, d] projection seen as
+    [B, H, N, d] among them; outputs are contiguous."""
+
+    def __init__(self, B: int, H: int, N: int, d: int, *, dtype: torch.dtype = torch.bfloat16, eps: float = 1e-6,
+                 quantize: int = 0, keep_y: bool = False, with_grad: bool = False, device="cuda"):
+        if dtype not in _DTYPE:
+            raise ValueError(f"unsupported dtype {dtype}")
+        if quantize not in (0, 1, 64, 128) or (quantize > 1 and d not in (64, 128)):
+            raise ValueError("quantize is 0, 1, or 64 or 128 rows of d = 64 or 128")
+        if with_grad and quantize and not keep_y:
+            raise ValueError("the e4m3 codes have no gradient: keep_y gives one to y")
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.B, self.H, self.N, self.d, self.dtype, self.device = B, H, N, d, dtype, dev
+        self.eps, self.quantize, self.keep_y, self.with_grad = eps, quantize, keep_y or not quantize, with_grad
+        need = vsa_rms_norm_bwd_workspace_size(self._shape())
+        if need == 0:
+            raise VsaError(_lib.VSA_ERR_INVALID_ARG, "vsa_rms_norm_bwd_workspace_size")
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev) if with_grad else None
+
+    def _shape(self, x=None, residual=None):
+        strides = [(0, 0, 0) if t is None or t.is_contiguous() else t.stride()[:3] for t in (x, residual)]
+        return make_norm_shape(self.B, self.H, self.N, self.d, *strides, block=max(self.quantize, 1), eps=self.eps)
+
+    def _rows(self, t: torch.Tensor, what: str, dense: bool = False) -> torch.Tensor:
+        shape = (self.B, self.H, self.N, self.d)
+        if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != shape:
+            raise ValueError(f"{what} is a {self.dtype} tensor of shape {shape} on {self.device}")
+        if (self.d > 1 and t.stride(3) != 1) or (dense and not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous" if dense else f"the last dimension of {what} must be dense")
+        # three zero strides are how the library is told of contiguous rows
+        return t.contiguous() if not any(t.stride()[:3]) else t
+
+    def _weight(self, weight: Optional[torch.Tensor]) -> int:
+        if weight is None:
+            return VSA_F32
+        if weight.dtype not in _DTYPE or weight.device != self.device or tuple(weight.shape) != (self.d,) \
+                or not weight.is_contiguous():
+            raise ValueError(f"weight is a contiguous float32 or bfloat16 tensor of shape {(self.d,)} on {self.device}")
+        return _DTYPE[weight.dtype]
+
+    def __call__(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 stream=None) -> NormOut:
+        wt = self._weight(weight)
+        shape = (self.B, self.H, self.N, self.d)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            x = self._rows(x, "x")
+            residual = None if residual is None else self._rows(residual, "the residual")
+            new = lambda *sh, dtype: torch.empty(*sh, dtype=dtype, device=self.device)  # noqa: E731
+            out = NormOut(new(*shape, dtype=self.dtype) if self.keep_y else None,
+                          new(*shape, dtype=self.dtype) if residual is not None else None,
+                          new(*shape, dtype=torch.uint8) if self.quantize else None,
+                          new(*shape[:2], -(-self.N // self.quantize), dtype=torch.int32) if self.quantize else None,
+                          new(*shape[:3], dtype=torch.float32))
+            vsa_rms_norm(x, residual, _DTYPE[self.dtype], weight, wt, self._shape(x, residual), out.sum, out.y,
+                         out.codes, out.exps, out.rstd)
+        return out
+
+    def backward(self, dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                 d_sum: Optional[torch.Tensor] = None, stream=None):
+        """(dx, d_weight) of a call: s is its x, or its sum where it had a residual; dy and d_sum the gradients of
+        y and of sum.  dx is the residual's gradient too, and has s's order of dimensions where s fills its
+        memory (else it is contiguous); d_weight is fp32 (None without a weight).  Asynchronous on ``stream``; can be captured."""
+        if not self.with_grad:
+            raise ValueError("the plan was made without with_grad=True")
+        wt = self._weight(weight)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            dy = self._rows(dy, "dy", dense=True)
+            d_sum = None if d_sum is None else self._rows(d_sum, "d_sum", dense=True)
+            s = self._rows(s, "s")
+            if rstd.dtype != torch.float32 or rstd.device != self.device or not rstd.is_contiguous() \
+                    or tuple(rstd.shape) != (self.B, self.H, self.N):
+                raise ValueError("rstd is the float32 tensor the call returned")
+            shape = (self.B, self.H, self.N, self.d)
+            dx = (torch.empty_strided(shape, s.stride(), dtype=s.dtype, device=self.device) if _whole_rows(s)
+                  else torch.empty(shape, dtype=s.dtype, device=self.device))
+            dw = torch.empty(self.d, dtype=torch.float32, device=self.device) if weight is not None else None
+            vsa_rms_norm_bwd(dy, d_sum, s, _DTYPE[self.dtype], weight, wt, rstd, self._shape(s, dx), dx, dw, self.ws,
+                             self.ws.numel())
+        return dx, dw
+
+    def normalise(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None):
+        """The call as a differentiable function of x, weight and residual: y, or (y, sum) with a residual.  As
+        SparseAttention.attend, refused under graph capture where autograd records it."""
+        if not self.with_grad:
+            raise ValueError("the plan was made without with_grad=True")
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual)):
+            _no_capture("normalise")
+        return _Normalise.apply(self, x, weight, residual)
+
+
+def _whole_rows(t: torch.Tensor) -> bool:
+    """Whether no two rows of t overlap and together they fill one piece of memory."""
+    span = t.shape[3]
+    for stride, size in sorted((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1):
+        if stride != span:
+            return False
+        span *= size
+    return True
+
+
 def attention(q, k, v, F: int, Hl: int, Wl: int, **kw):
     """Convenience wrapper: build a :class:`SparseAttention` for q's shape and run it once."""
     B, H, N, d = q.shape
@@ -368,5 +513,7 @@ __all__ = ["SparseAttention", "SemanticAttention", "attention", "SemParams", "ma
            "vsa_pattern_window", "vsa_permute", "vsa_profile_heads", "vsa_profile_rows",
            "vsa_profile_workspace_size", "vsa_sparse_attn_fwd", "vsa_sparse_attn_fwd_natural", "vsa_unpermute",
            "vsa_quantize_fp8", "vsa_sparse_attn_fwd_fp8qk", "QKVOGrad", "qkvo_grad", "vsa_sparse_attn_bwd",
-           "vsa_sparse_attn_bwd_workspace_size", "vsa_attention_bwd", "vsa_attention_bwd_workspace_size", "VSA_SPATIAL", "VSA_TEMPORAL",
+           "vsa_sparse_attn_bwd_workspace_size", "vsa_attention_bwd", "vsa_attention_bwd_workspace_size",
+           "RMSNorm", "NormOut", "NormShape", "make_norm_shape", "vsa_rms_norm", "vsa_rms_norm_bwd",
+           "vsa_rms_norm_bwd_workspace_size", "VSA_SPATIAL", "VSA_TEMPORAL",
            "VSA_CUBE", "VSA_F32", "VSA_BF16", "VSA_SELECT_PROFILE", "VSA_SELECT_GIVEN", "VSA_SELECT_CUBE"]

@@ -60,6 +60,12 @@ class QKVOGrad(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "d_o", "lse", "d_lse", "dq", "dk", "dv")]
 
 
+class NormShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
+                ("x_stride", ctypes.c_int64 * 3), ("res_stride", ctypes.c_int64 * 3), ("block", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libvsa.so is not built ({LIB_PATH}); run `python block_sparse_attention_31_b200/build.py`")
@@ -98,6 +104,9 @@ def _load():
                                      vp]),
         "vsa_attention_bwd_workspace_size": (sz, [P(Shape), P(Params), i32]),
         "vsa_attention_bwd": (st, [P(QKVOGrad), i32, P(Shape), P(Params), vp, vp, sz, vp, vp]),
+        "vsa_rms_norm": (st, [vp, vp, i32, vp, i32, P(NormShape), vp, vp, vp, vp, vp, vp]),
+        "vsa_rms_norm_bwd_workspace_size": (sz, [P(NormShape)]),
+        "vsa_rms_norm_bwd": (st, [vp, vp, vp, i32, vp, i32, vp, P(NormShape), vp, vp, vp, sz, vp]),
         "vsa_get_device_error": (st, [vp, vp, P(i32)]),
         "vsa_kmeans_workspace_size": (sz, [P(Shape), i32]),
         "vsa_kmeans": (st, [vp, P(Shape), i32, i32, vp, vp, vp, vp, vp, sz, vp, vp]),
@@ -338,6 +347,32 @@ def vsa_attention_bwd_workspace_size(shape: Shape, params: Params, dtype: int) -
 def vsa_attention_bwd(io: QKVOGrad, dtype: int, shape: Shape, params: Params, kinds, ws, ws_bytes, err, stream=None):
     _check(lib.vsa_attention_bwd(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
                                  _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention_bwd")
+
+
+# ---------------------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------------------
+
+def make_norm_shape(B, H, N, d, x_stride=(0, 0, 0), res_stride=(0, 0, 0), block=1, eps=1e-6) -> NormShape:
+    i3 = ctypes.c_int64 * 3
+    return NormShape(int(B), int(H), int(N), int(d), i3(*x_stride), i3(*res_stride), int(block), float(eps))
+
+
+def vsa_rms_norm(x, residual, dtype: int, weight, weight_dtype: int, shape: NormShape, sum=None, y=None, codes=None,
+                 exps=None, rstd=None, stream=None):
+    _check(lib.vsa_rms_norm(_ptr(x), _ptr(residual), dtype, _ptr(weight), weight_dtype, ctypes.byref(shape), _ptr(sum),
+                            _ptr(y), _ptr(codes), _ptr(exps), _ptr(rstd), _stream(stream)), "vsa_rms_norm")
+
+
+def vsa_rms_norm_bwd_workspace_size(shape: NormShape) -> int:
+    return int(lib.vsa_rms_norm_bwd_workspace_size(ctypes.byref(shape)))
+
+
+def vsa_rms_norm_bwd(dy, d_sum, s, dtype: int, weight, weight_dtype: int, rstd, shape: NormShape, dx, d_weight=None,
+                     ws=None, ws_bytes=0, stream=None):
+    _check(lib.vsa_rms_norm_bwd(_ptr(dy), _ptr(d_sum), _ptr(s), dtype, _ptr(weight), weight_dtype, _ptr(rstd),
+                                ctypes.byref(shape), _ptr(dx), _ptr(d_weight), _ptr(ws), int(ws_bytes),
+                                _stream(stream)), "vsa_rms_norm_bwd")
 
 
 def vsa_get_device_error(err, stream=None) -> int:

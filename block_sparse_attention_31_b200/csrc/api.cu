@@ -668,6 +668,127 @@ vsa_status vsa_sparse_attn_bwd(const vsa_qkvo_grad* natural, const vsa_qkvo_grad
 }
 
 // ---------------------------------------------------------------------------------------
+// Root-mean-square norm
+// ---------------------------------------------------------------------------------------
+static bool known_dtype(vsa_dtype t) { return t == VSA_F32 || t == VSA_BF16; }
+
+static bool on_elements(const void* p, vsa_dtype t) {
+  return reinterpret_cast<uintptr_t>(p) % (t == VSA_F32 ? 4 : 2) == 0;
+}
+
+// Strides of a [B, H, N] array of rows: as given, or contiguous where all three are 0.
+static vsa_status norm_strides(const vsa_norm_shape* s, const int64_t (&given)[3], int64_t (&out)[3]) {
+  const int64_t most = INT64_C(1) << 46, size[3] = {s->B, s->H, s->N};
+  for (int i = 0; i < 3; ++i)
+    if (given[i] < 0 || given[i] > most / size[i]) return VSA_ERR_INVALID_ARG;
+  const bool contiguous = given[0] == 0 && given[1] == 0 && given[2] == 0;
+  const int64_t d = s->d;
+  out[0] = contiguous ? d * s->N * s->H : given[0];
+  out[1] = contiguous ? d * s->N : given[1];
+  out[2] = contiguous ? d : given[2];
+  return VSA_OK;
+}
+
+static vsa_status norm_args(const vsa_norm_shape* s, NormArgs* a) {
+  if (s == nullptr) return VSA_ERR_INVALID_ARG;
+  if (s->B <= 0 || s->H <= 0 || s->N <= 0 || s->d <= 0 || !(s->eps >= 0.f) || !std::isfinite(s->eps))
+    return VSA_ERR_INVALID_ARG;
+  if (s->d > 16384 || s->N > (1 << 28)) return VSA_ERR_UNSUPPORTED;
+  const long long heads = static_cast<long long>(s->B) * s->H;
+  if (heads > 0x7fffffffLL || heads * s->N > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;  // one CTA per row at most
+  vsa_status st;
+  if ((st = norm_strides(s, s->x_stride, a->x_stride)) != VSA_OK) return st;
+  if ((st = norm_strides(s, s->res_stride, a->res_stride)) != VSA_OK) return st;
+  a->BH = static_cast<int>(heads);
+  a->H = s->H;
+  a->N = s->N;
+  a->d = s->d;
+  a->block = 1;
+  a->eps = s->eps;
+  return VSA_OK;
+}
+
+vsa_status vsa_rms_norm(const void* x, const void* residual, vsa_dtype dtype, const void* weight,
+                        vsa_dtype weight_dtype, const vsa_norm_shape* shape, void* sum, void* y, uint8_t* codes,
+                        int32_t* d_exp, float* rstd, cudaStream_t stream) {
+  NormArgs a{};
+  vsa_status st = norm_args(shape, &a);
+  if (st != VSA_OK) return st;
+  if (!x || !known_dtype(dtype) || (weight && !known_dtype(weight_dtype))) return VSA_ERR_INVALID_ARG;
+  if (!y && !codes) return VSA_ERR_INVALID_ARG;
+  if ((sum && !residual) || (codes == nullptr) != (d_exp == nullptr)) return VSA_ERR_INVALID_ARG;
+  if (!on_elements(x, dtype) || !on_elements(residual, dtype)) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(weight) || !aligned16(sum) || !aligned16(y) || !aligned16(codes) || !aligned16(d_exp) ||
+      !aligned16(rstd))
+    return VSA_ERR_INVALID_ARG;
+  for (const void* out : {static_cast<const void*>(sum), static_cast<const void*>(y), static_cast<const void*>(codes)})
+    if (out && (out == x || out == residual || out == weight)) return VSA_ERR_INVALID_ARG;
+  if (sum && (sum == y || sum == codes)) return VSA_ERR_INVALID_ARG;
+  if (codes) {
+    if (shape->block != 1 && shape->block != 64 && shape->block != 128) return VSA_ERR_UNSUPPORTED;
+    if (shape->block > 1 && shape->d != 64 && shape->d != 128) return VSA_ERR_UNSUPPORTED;
+    a.block = shape->block;
+  }
+  if (!on_current_device({x, residual, weight, sum, y, codes, d_exp, rstd})) return VSA_ERR_INVALID_ARG;
+  a.x = x;
+  a.res = residual;
+  a.w = weight;
+  a.w_f32 = weight_dtype == VSA_F32;
+  a.sum = sum;
+  a.y = y;
+  a.codes = codes;
+  a.exps = d_exp;
+  a.rstd = rstd;
+  return launch_rms_norm(a, dtype == VSA_F32, stream) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape* shape) {
+  NormArgs a{};
+  if (norm_args(shape, &a) != VSA_OK) return 0;
+  const long long rows = static_cast<long long>(a.BH) * a.N;
+  return align256(static_cast<size_t>(std::min<long long>(rows, kNormBwdCtas)) * a.d * 4);
+}
+
+vsa_status vsa_rms_norm_bwd(const void* dy, const void* d_sum, const void* s, vsa_dtype dtype, const void* weight,
+                            vsa_dtype weight_dtype, const float* rstd, const vsa_norm_shape* shape, void* dx,
+                            float* d_weight, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  NormBwdArgs a{};
+  vsa_status st = norm_args(shape, &a.n);
+  if (st != VSA_OK) return st;
+  if (!dy || !s || !rstd || !dx || !known_dtype(dtype) || (weight && !known_dtype(weight_dtype)))
+    return VSA_ERR_INVALID_ARG;
+  if (!on_elements(s, dtype) || !on_elements(dx, dtype) || !aligned16(dy) || !aligned16(d_sum) || !aligned16(weight) ||
+      !aligned16(rstd) || !aligned16(d_weight) || !aligned16(ws))
+    return VSA_ERR_INVALID_ARG;
+  if (dx == dy || dx == d_sum || dx == s) return VSA_ERR_INVALID_ARG;
+  // rows of dx must not overlap: each stride has to step over everything the smaller ones span
+  struct {
+    int64_t stride, size;
+  } dims[3] = {{a.n.res_stride[0], shape->B}, {a.n.res_stride[1], shape->H}, {a.n.res_stride[2], shape->N}};
+  std::sort(dims, dims + 3, [](const auto& p, const auto& q) { return p.stride < q.stride; });
+  int64_t span = a.n.d;
+  for (const auto& m : dims) {
+    if (m.size == 1) continue;
+    if (m.stride < span) return VSA_ERR_INVALID_ARG;
+    span += m.stride * (m.size - 1);
+  }
+  if (d_weight) {
+    if (!ws) return VSA_ERR_INVALID_ARG;
+    if (ws_bytes < vsa_rms_norm_bwd_workspace_size(shape)) return VSA_ERR_WORKSPACE;
+  }
+  if (!on_current_device({dy, d_sum, s, weight, rstd, dx, d_weight, d_weight ? ws : nullptr})) return VSA_ERR_INVALID_ARG;
+  a.n.x = s;
+  a.n.w = weight;
+  a.n.w_f32 = weight_dtype == VSA_F32;
+  a.n.rstd = const_cast<float*>(rstd);
+  a.dy = dy;
+  a.d_sum = d_sum;
+  a.dx = dx;
+  a.partial = d_weight ? static_cast<float*>(ws) : nullptr;
+  return launch_rms_norm_bwd(a, dtype == VSA_F32, d_weight, stream) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------------------
 // Semantic-aware permutation ("Sparse VideoGen2" page, abstract)
 // ---------------------------------------------------------------------------------------
 // Shapes of the semantic path: no cube dims (every head has N rows).

@@ -52,10 +52,10 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl == 384 * 168, "register sp
 
 template <int D, int BN, bool kKey>
 struct BwdCfg {
-  // Ring stages of X (Q or K) and Y (dO or V).  A tile takes about 1500 cycles to arrive; with a spare
-  // stage of each no product waits for it.  The
-  // spare X stage is given up where the bitset of a very long head needs its place.
-  [[maybe_unused]] static constexpr int NX_MOST = 3, NX_LEAST = 2, NY = 2, NT = 2;
+  // Ring stages of X (Q or K) and Y (dO or V) and of the rows' terms.  A tile takes about 1500 cycles to
+  // arrive; with a spare stage of each no product waits for it.  The spare X stage is given up where the
+  // bitset of a very long head needs its place.
+  static constexpr int NX_MOST = 3, NY = 2, NT = 2;
   static constexpr int A_BYTES = kBM * D * 2;             // a resident tile (M = 128 lanes, BN rows loaded)
   static constexpr int T_BYTES = BN * D * 2;              // a ring tile
   static constexpr int ST_BYTES = 2 * BN * 4;             // the rows' two terms of a block
@@ -79,7 +79,7 @@ struct BwdCfg {
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(kBM, BN, false, false);
   static constexpr uint32_t IDESC_G = idesc_bf16_f32(kBM, D, false, true);
   static int smem_bytes(int nx, int nwords) { return OFF_X + nx * T_BYTES + OFF_BITS + 4 * nwords; }
-  static int stages(int nwords) { return smem_bytes(NX_MOST, nwords) <= kMaxSmem ? NX_MOST : NX_LEAST; }
+  static int stages(int nwords) { return smem_bytes(NX_MOST, nwords) <= kMaxSmem ? NX_MOST : NX_MOST - 1; }
 };
 
 enum {
@@ -695,7 +695,7 @@ cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cud
 
 bool sparse_attn_bwd_fits(const Geom& g, int BH) {
   using C = BwdCfg<128, 128, true>;
-  return C::smem_bytes(C::NX_LEAST, (g.nblk + 31) / 32) <= kMaxSmem &&
+  return C::smem_bytes(C::NX_MOST - 1, (g.nblk + 31) / 32) <= kMaxSmem &&
          2LL * BH * g.nblk <= 0x7fffffffLL && static_cast<long long>(BH) * g.nblk * g.block / 8 <= 0x7fffffffLL;
 }
 

@@ -5,25 +5,16 @@
 // `block` rows of a head's layout, the smallest with max |x| <= 448 * 2^e (e = 0 for an
 // all-zero block).  The attention multiplies each block pair's scores by 2^(e_q + e_k).
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
 
 namespace vsa {
 
 constexpr int kQuantThreads = 512;
-
-// Smallest e with a <= 448 * 2^e for a > 0: with a = f * 2^E, f in [0.5, 1), and
-// 448 = 0.875 * 2^9, that is E - 9 when f <= 0.875 and E - 8 otherwise.
-__device__ __forceinline__ int e4m3_block_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  int E;
-  const float f = frexpf(amax, &E);
-  return f <= 0.875f ? E - 9 : E - 8;
-}
 
 // One CTA per (head, block of BN rows of the head's layout): the block's max |x|, its
 // exponent, then the codes.  Rows past the head's own rows are written as zeros.
@@ -72,10 +63,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_e4m3_kernel(const __nv
   for (int w = 1; w < kQuantThreads / 32; ++w) m = fmaxf(m, red[w]);
   const int e = e4m3_block_exponent(m);
   if (tid == 0) exps[static_cast<size_t>(bh) * g.nblk + b] = e;
-  // 2^-e as a float (exact for -126 <= -e <= 127; other exponents go through ldexpf)
-  const bool plain = e >= -127 && e <= 126;
-  const float inv = plain ? __int_as_float((127 - e) << 23) : 1.f;
-  auto scaled = [&](float x) { return plain ? x * inv : ldexpf(x, -e); };
+  const E4m3Scale scaled(e);
   // x / 2^e is exact (a power-of-two scaling of a bf16 value); the conversion rounds to the
   // nearest e4m3 value, ties to even, saturating at 448
 #pragma unroll
@@ -88,9 +76,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_e4m3_kernel(const __nv
       const float x0 = scaled(__uint_as_float(w[2 * h] << 16)), x1 = scaled(__uint_as_float(w[2 * h] & 0xffff0000u));
       const float x2 = scaled(__uint_as_float(w[2 * h + 1] << 16)),
                   x3 = scaled(__uint_as_float(w[2 * h + 1] & 0xffff0000u));
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, __NV_E4M3);
-      packed[h] = (lo & 0xffffu) | (hi << 16);
+      packed[h] = e4m3_pair(x0, x1) | (e4m3_pair(x2, x3) << 16);
     }
     if (b * BN + c / (D / 8) < g.R)  // the last block of a head may reach past its R rows
       *reinterpret_cast<uint2*>(out + static_cast<size_t>(c / (D / 8)) * D + (c % (D / 8)) * 8) =

@@ -138,6 +138,32 @@ cudaError_t launch_profile(const void* q, const void* k, const void* v, const Ge
                            int w_t, float scale_log2, const ProfilePlan& plan, void* ws, uint8_t* kinds_out,
                            float* mse_out, int* err, cudaStream_t stream);
 
+// Root-mean-square norm of rows (norm.cu): B*H heads of N rows of d elements, outputs contiguous.
+struct NormArgs {
+  const void *x, *res;      // rows at b * stride[0] + h * stride[1] + n * stride[2]; res may be null
+  const void* w;            // d weights, or null for ones
+  void *sum, *y;            // either may be null
+  uint8_t* codes;           // e4m3 codes with their exponents, or null
+  int32_t* exps;
+  float* rstd;              // written (may be null); read by the gradient
+  int64_t x_stride[3], res_stride[3];
+  int w_f32;
+  int BH, H, N, d;
+  int block;                // rows per exponent
+  int chunks;               // chunks of rows per head, set by the launcher
+  float eps;
+};
+struct NormBwdArgs {
+  NormArgs n;               // x: the normalised rows' input (the sum), rstd, weights, shape; res_stride: dx's
+  const void *dy, *d_sum;   // contiguous; d_sum may be null
+  void* dx;
+  float* partial;           // [CTAs, d] fp32, or null when dw is not wanted
+};
+// CTAs of the gradient (and rows of its workspace): four for each of 148 SMs.
+constexpr int kNormBwdCtas = 592;
+cudaError_t launch_rms_norm(NormArgs a, bool f32, cudaStream_t stream);
+cudaError_t launch_rms_norm_bwd(NormBwdArgs a, bool f32, float* dw, cudaStream_t stream);
+
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 cudaError_t encode_rows_map(CUtensorMap* map, const void* base, int d, int rows, int BH, int box_rows);
 // The same for rows of d = 128 one-byte elements (e4m3 codes): one 128-byte box per row.

@@ -435,6 +435,63 @@ VSA_API vsa_status vsa_attention_bwd(const vsa_qkvo_grad *io, vsa_dtype dtype, c
                                      int *d_err, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Root-mean-square norm of rows (no counterpart in the pages; the transformers they speed up
+ * normalise Q and K in front of the attention) and its gradient.
+ * ------------------------------------------------------------------------------------- */
+
+typedef struct {
+    int B, H, N;                  /* rows: [B, H, N] of d elements each */
+    int d;                        /* 1 .. 16384 */
+    int64_t x_stride[3];          /* elements between rows of x along B, H, N; all 0: contiguous.  A
+                                     [B, N, H, d] projection is read in place: N*H*d, d, H*d */
+    int64_t res_stride[3];        /* the residual's, likewise */
+    int block;                    /* rows per exponent of the codes: 1, or 64 or 128 consecutive rows of a head
+                                     (d = 64 or 128 then), as vsa_quantize_fp8 groups them */
+    float eps;                    /* >= 0 */
+} vsa_norm_shape;
+
+/*
+ * s = x + residual, rstd = 1 / sqrt(mean(s^2) + eps), y = s * rstd * weight, in fp32; y is taken from
+ * s before s is rounded.
+ *   x, residual  rows in dtype (VSA_F32 or VSA_BF16), strided; residual may be NULL (s = x).  Rows whose
+ *                pointers and strides are multiples of 16 bytes are read 16 bytes at a time, others
+ *                element by element
+ *   weight       [d] in weight_dtype, or NULL for ones
+ *   sum          [B, H, N, d] dtype out: s, or NULL (needs a residual)
+ *   y            [B, H, N, d] dtype out, or NULL
+ *   codes        [B, H, N, d] e4m3 codes of y / 2^e out, or NULL: nearest even, with one exponent e per
+ *                `block` rows, the smallest with max |y| <= 448 * 2^e (0 for all-zero rows), in the
+ *                layout vsa_sparse_attn_fwd_fp8qk takes.  y is not rounded to dtype in between.
+ *                A NaN has the NaN code; an infinity is saturated, with e = 120
+ *   d_exp        [B*H, ceil(N / block)] int32 out (with codes)
+ *   rstd         [B, H, N] fp32 out, or NULL
+ * Outputs are contiguous, overlap no input, and at least one of y and codes is given.
+ */
+VSA_API vsa_status vsa_rms_norm(const void *x, const void *residual, vsa_dtype dtype, const void *weight,
+                                vsa_dtype weight_dtype, const vsa_norm_shape *shape, void *sum, void *y,
+                                uint8_t *codes, int32_t *d_exp, float *rstd, cudaStream_t stream);
+
+/* Workspace bytes of vsa_rms_norm_bwd with d_weight (up to 592 partial sums of d fp32); 0 for an
+ * invalid shape. */
+VSA_API size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape *shape);
+
+/*
+ * Gradient of vsa_rms_norm: with xh = s * rstd and g = dy * weight,
+ *   dx = rstd * (g - xh * mean(g * xh)) + d_sum,   d_weight = sum over rows of dy * xh (fp32).
+ * dx is the gradient of x and of the residual alike.
+ *   s            the forward call's x, or its sum where it had a residual; rows at x_stride
+ *   dy, d_sum    [B, H, N, d] dtype, contiguous: gradients of y and of sum; d_sum may be NULL
+ *   rstd         the forward call's
+ *   dx           out, dtype, rows at res_stride (which must not make two rows overlap)
+ *   d_weight     [d] fp32 out, or NULL; with it ws holds vsa_rms_norm_bwd_workspace_size bytes.  The
+ *                sums have a fixed order: two runs give the same bits
+ */
+VSA_API vsa_status vsa_rms_norm_bwd(const void *dy, const void *d_sum, const void *s, vsa_dtype dtype,
+                                    const void *weight, vsa_dtype weight_dtype, const float *rstd,
+                                    const vsa_norm_shape *shape, void *dx, float *d_weight, void *ws,
+                                    size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Semantic-aware permutation ("Sparse VideoGen2" page, abstract: tokens clustered by
  * k-means and reordered by cluster, a top-p budget over clusters).  The page gives no
  * formulas; the readings:

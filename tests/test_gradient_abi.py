@@ -94,3 +94,40 @@ def test_reference_gradient_matches_differences(seed):
         up[i], down[i] = up[i] + e * u, down[i] - e * u
         # central differences: an error of order e^2 of third derivatives of order one, and 1e-16 * |loss| / e
         assert (loss(up) - loss(down)) / (2 * e) == pytest.approx(float((grads[i] * u).sum()), rel=1e-6, abs=1e-7)
+
+
+def test_norm_refused_before_launch():
+    lib, good = _lib.lib, dict(B=1, H=2, N=10, d=64)
+
+    def fwd(shape=good, x=FAKE, res=None, dtype=1, w=FAKE, wt=1, sum=None, y=FAKE + 192, codes=None, exps=None, rstd=FAKE, **kw):
+        sh = _lib.make_norm_shape(**{**shape, **kw})
+        return lib.vsa_rms_norm(x, res, dtype, w, wt, ctypes.byref(sh), sum, y, codes, exps, rstd, s)
+
+    def bwd(shape=good, dy=FAKE, d_sum=None, x=FAKE + 64, dtype=1, w=FAKE, wt=0, rstd=FAKE, dx=FAKE + 128, dw=FAKE, ws=FAKE, wsb=1 << 30,
+            **kw):
+        sh = _lib.make_norm_shape(**{**shape, **kw})
+        return lib.vsa_rms_norm_bwd(dy, d_sum, x, dtype, w, wt, rstd, ctypes.byref(sh), dx, dw, ws, wsb, s)
+
+    inv, uns = _lib.VSA_ERR_INVALID_ARG, _lib.VSA_ERR_UNSUPPORTED
+    for bad in (dict(B=0), dict(H=-1), dict(N=0), dict(d=0), dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")),
+                dict(x_stride=(1, -1, 1)), dict(res_stride=(1 << 50, 1, 1))):
+        assert fwd(**bad) == inv and bwd(**bad) == inv
+        assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(**{**good, **bad})) == 0
+    for bad in (dict(d=16385), dict(B=1 << 20, H=1 << 20), dict(B=1 << 10, H=1 << 10, N=1 << 12)):
+        assert fwd(**bad) == uns and bwd(**bad) == uns
+    assert fwd(x=None) == inv and fwd(x=FAKE + 1) == inv and fwd(dtype=2) == inv and fwd(wt=5) == inv
+    assert fwd(y=None) == inv                                       # nothing to write
+    assert fwd(sum=FAKE + 64) == inv                                # a sum needs a residual
+    assert fwd(codes=FAKE + 64) == inv and fwd(exps=FAKE) == inv    # codes and exponents go together
+    assert fwd(y=FAKE + 2) == inv and fwd(w=FAKE + 4) == inv and fwd(rstd=FAKE + 4) == inv
+    assert fwd(x=FAKE + 64, y=FAKE + 64) == inv                     # in place
+    assert fwd(res=FAKE + 64, sum=FAKE + 64) == inv
+    assert fwd(codes=FAKE + 64, exps=FAKE, block=32) == uns
+    assert fwd(codes=FAKE + 64, exps=FAKE, block=64, d=96) == uns
+    assert bwd(dy=None) == inv and bwd(x=None) == inv and bwd(rstd=None) == inv and bwd(dx=None) == inv
+    assert bwd(dx=FAKE) == inv and bwd(dx=FAKE + 64) == inv         # in place
+    assert bwd(ws=None) == inv and bwd(wsb=8) == _lib.VSA_ERR_WORKSPACE
+    assert bwd(res_stride=(0, 64, 32)) == inv                       # rows of dx that overlap
+    assert bwd(res_stride=(0, 0, 64)) == inv                        # heads of dx that coincide
+    assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(**good)) == 20 * 64 * 4
+    assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(1, 1, 10000, 100)) == -(-592 * 100 * 4 // 256) * 256
