@@ -412,7 +412,7 @@ class RMSNorm:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.B, self.H, self.N, self.d, self.dtype, self.device = B, H, N, d, dtype, dev
         self.eps, self.quantize, self.keep_y, self.with_grad = eps, quantize, keep_y or not quantize, with_grad
-        need = vsa_rms_norm_bwd_workspace_size(self._shape())
+        need = vsa_rms_norm_bwd_workspace_size(self._shape(), _DTYPE[dtype])
         if need == 0:
             raise VsaError(_lib.VSA_ERR_INVALID_ARG, "vsa_rms_norm_bwd_workspace_size")
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev) if with_grad else None

@@ -105,7 +105,7 @@ def _load():
         "vsa_attention_bwd_workspace_size": (sz, [P(Shape), P(Params), i32]),
         "vsa_attention_bwd": (st, [P(QKVOGrad), i32, P(Shape), P(Params), vp, vp, sz, vp, vp]),
         "vsa_rms_norm": (st, [vp, vp, i32, vp, i32, P(NormShape), vp, vp, vp, vp, vp, vp]),
-        "vsa_rms_norm_bwd_workspace_size": (sz, [P(NormShape)]),
+        "vsa_rms_norm_bwd_workspace_size": (sz, [P(NormShape), i32]),
         "vsa_rms_norm_bwd": (st, [vp, vp, vp, i32, vp, i32, vp, P(NormShape), vp, vp, vp, sz, vp]),
         "vsa_get_device_error": (st, [vp, vp, P(i32)]),
         "vsa_kmeans_workspace_size": (sz, [P(Shape), i32]),
@@ -364,8 +364,8 @@ def vsa_rms_norm(x, residual, dtype: int, weight, weight_dtype: int, shape: Norm
                             _ptr(y), _ptr(codes), _ptr(exps), _ptr(rstd), _stream(stream)), "vsa_rms_norm")
 
 
-def vsa_rms_norm_bwd_workspace_size(shape: NormShape) -> int:
-    return int(lib.vsa_rms_norm_bwd_workspace_size(ctypes.byref(shape)))
+def vsa_rms_norm_bwd_workspace_size(shape: NormShape, dtype: int) -> int:
+    return int(lib.vsa_rms_norm_bwd_workspace_size(ctypes.byref(shape), dtype))
 
 
 def vsa_rms_norm_bwd(dy, d_sum, s, dtype: int, weight, weight_dtype: int, rstd, shape: NormShape, dx, d_weight=None,

@@ -733,7 +733,7 @@ vsa_status vsa_rms_norm(const void* x, const void* residual, vsa_dtype dtype, co
   a.x = x;
   a.res = residual;
   a.w = weight;
-  a.w_f32 = weight_dtype == VSA_F32;
+  a.w_kind = weight == nullptr ? 0 : weight_dtype == VSA_F32 ? 1 : 2;
   a.sum = sum;
   a.y = y;
   a.codes = codes;
@@ -742,11 +742,10 @@ vsa_status vsa_rms_norm(const void* x, const void* residual, vsa_dtype dtype, co
   return launch_rms_norm(a, dtype == VSA_F32, stream) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
-size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape* shape) {
+size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape* shape, vsa_dtype dtype) {
   NormArgs a{};
-  if (norm_args(shape, &a) != VSA_OK) return 0;
-  const long long rows = static_cast<long long>(a.BH) * a.N;
-  return align256(static_cast<size_t>(std::min<long long>(rows, kNormBwdCtas)) * a.d * 4);
+  if (norm_args(shape, &a) != VSA_OK || !known_dtype(dtype)) return 0;
+  return align256(rms_norm_bwd_partials(static_cast<long long>(a.BH) * a.N, a.d, dtype == VSA_F32) * a.d * 4);
 }
 
 vsa_status vsa_rms_norm_bwd(const void* dy, const void* d_sum, const void* s, vsa_dtype dtype, const void* weight,
@@ -774,12 +773,12 @@ vsa_status vsa_rms_norm_bwd(const void* dy, const void* d_sum, const void* s, vs
   }
   if (d_weight) {
     if (!ws) return VSA_ERR_INVALID_ARG;
-    if (ws_bytes < vsa_rms_norm_bwd_workspace_size(shape)) return VSA_ERR_WORKSPACE;
+    if (ws_bytes < vsa_rms_norm_bwd_workspace_size(shape, dtype)) return VSA_ERR_WORKSPACE;
   }
   if (!on_current_device({dy, d_sum, s, weight, rstd, dx, d_weight, d_weight ? ws : nullptr})) return VSA_ERR_INVALID_ARG;
   a.n.x = s;
   a.n.w = weight;
-  a.n.w_f32 = weight_dtype == VSA_F32;
+  a.n.w_kind = weight == nullptr ? 0 : weight_dtype == VSA_F32 ? 1 : 2;
   a.n.rstd = const_cast<float*>(rstd);
   a.dy = dy;
   a.d_sum = d_sum;

@@ -5,25 +5,26 @@
 
 namespace vsa {
 
-// Smallest e with a <= 448 * 2^e for a > 0: with a = f * 2^E, f in [0.5, 1), and
-// 448 = 0.875 * 2^9, that is E - 9 when f <= 0.875 and E - 8 otherwise.
-__device__ __forceinline__ int e4m3_block_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  int E;
-  const float f = frexpf(amax, &E);
-  return f <= 0.875f ? E - 9 : E - 8;
+// Smallest e with a <= 448 * 2^e for a > 0 (0 for 0): 448 = 1.75 * 2^8, so e is a's exponent - 8, one more
+// when a's mantissa is above 1.75.
+__device__ __forceinline__ int e4m3_block_exponent(float a) {
+  if (!(a > 0.f)) return 0;
+  const bool small = a < 1.17549435e-38f;  // subnormal: scaled up by 2^32
+  const int bits = __float_as_int(small ? a * 4294967296.f : a);
+  return ((bits + 0x1fffff) >> 23) - 135 - (small ? 32 : 0);
 }
 
-// Division by 2^e, exact but for results below the normal range.
+// Division by 2^e for |e| < 252 as one or two products with normal powers of two (2^-e itself may be out of
+// range).  Exact for every result that is not far below the smallest code.
 struct E4m3Scale {
-  float inv;
-  int e;
-  bool plain;  // 2^-e is a normal float
-  __device__ explicit E4m3Scale(int exponent)
-      : inv(1.f), e(exponent), plain(exponent >= -127 && exponent <= 126) {
-    if (plain) inv = __int_as_float((127 - e) << 23);
+  float a, b;
+  bool twice;
+  __device__ explicit E4m3Scale(int e) : twice(e < -126 || e > 126) {
+    const int h = twice ? e / 2 : e;
+    a = __int_as_float((127 - h) << 23);
+    b = __int_as_float((127 - (e - h)) << 23);
   }
-  __device__ float operator()(float x) const { return plain ? x * inv : ldexpf(x, -e); }
+  __device__ float operator()(float x) const { return twice ? x * a * b : x * a; }
 };
 
 // Two codes (nearest even, saturating at 448), the first in the low byte.

@@ -147,7 +147,7 @@ struct NormArgs {
   int32_t* exps;
   float* rstd;              // written (may be null); read by the gradient
   int64_t x_stride[3], res_stride[3];
-  int w_f32;
+  int w_kind;               // 0 none, 1 fp32, 2 bf16
   int BH, H, N, d;
   int block;                // rows per exponent
   int chunks;               // chunks of rows per head, set by the launcher
@@ -159,8 +159,8 @@ struct NormBwdArgs {
   void* dx;
   float* partial;           // [CTAs, d] fp32, or null when dw is not wanted
 };
-// CTAs of the gradient (and rows of its workspace): four for each of 148 SMs.
-constexpr int kNormBwdCtas = 592;
+// Rows of d floats that the gradient's partial sums take at most.
+size_t rms_norm_bwd_partials(long long rows, int d, bool f32);
 cudaError_t launch_rms_norm(NormArgs a, bool f32, cudaStream_t stream);
 cudaError_t launch_rms_norm_bwd(NormBwdArgs a, bool f32, float* dw, cudaStream_t stream);
 

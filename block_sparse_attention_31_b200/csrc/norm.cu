@@ -8,8 +8,10 @@
 // Both are bound by memory: each row is read once into registers (16 bytes a load), reduced by the
 // threads that hold it, and written.  A row belongs to TPR threads of one warp, or to a whole CTA when
 // it is longer than a warp's registers hold; short rows are taken several at a time so that every
-// thread has several loads in flight.  All arithmetic is fp32; y, sum and dx are rounded once, when they are
-// written, and y is normalised from the sum before its rounding.
+// thread has several loads in flight.  At 6.5 TB/s an SM has some 12 instructions for an element, so the
+// arithmetic runs on packed pairs (f32x2) and a thread holds at least 16 elements of a row where it can:
+// what a row costs once (its reduction, root and exponent) is shared by them.  All arithmetic is fp32; y, sum and
+// dx are rounded once, when they are written, and y is normalised from the sum before its rounding.
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -22,8 +24,6 @@
 namespace vsa {
 
 namespace {
-
-constexpr int kCodesNone = 0, kCodesRow = 1, kCodesBlock = 2;
 
 // VEC consecutive elements of a row: 16 bytes, or one element where rows are not 16-byte aligned.
 template <typename T, int VEC>
@@ -74,15 +74,89 @@ struct Chunk<float, 1> {
   __device__ static void store(float* p, const float* f) { *p = f[0]; }
 };
 
+// ---- arithmetic on the N elements of a chunk, two at a time where N is even ----
+template <int N>
+__device__ __forceinline__ void v_scale(float* f, float c) {
+  if constexpr (N % 2 == 0) {
+    const uint64_t c2 = f2_make(c, c);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) f2_split(f2_mul(f2_make(f[i], f[i + 1]), c2), f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] *= c;
+  }
+}
+template <int N>
+__device__ __forceinline__ void v_mul(float* f, const float* w) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) f2_split(f2_mul(f2_make(f[i], f[i + 1]), f2_make(w[i], w[i + 1])), f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] *= w[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void v_add(float* f, const float* o) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) f2_split(f2_add(f2_make(f[i], f[i + 1]), f2_make(o[i], o[i + 1])), f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] += o[i];
+  }
+}
+// f = a * b + f
+template <int N>
+__device__ __forceinline__ void v_fma(float* f, const float* a, const float* b) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      f2_split(f2_fma(f2_make(a[i], a[i + 1]), f2_make(b[i], b[i + 1]), f2_make(f[i], f[i + 1])), f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fmaf(a[i], b[i], f[i]);
+  }
+}
+template <int N>
+__device__ __forceinline__ float v_dot(const float* a, const float* b) {
+  if constexpr (N % 2 == 0) {
+    uint64_t s = f2_mul(f2_make(a[0], a[1]), f2_make(b[0], b[1]));
+#pragma unroll
+    for (int i = 2; i < N; i += 2) s = f2_fma(f2_make(a[i], a[i + 1]), f2_make(b[i], b[i + 1]), s);
+    float lo, hi;
+    f2_split(s, lo, hi);
+    return lo + hi;
+  } else {
+    float s = a[0] * b[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) s = fmaf(a[i], b[i], s);
+    return s;
+  }
+}
+template <int N>
+__device__ __forceinline__ float v_top(const float* f, float top) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) top = fmax3(top, fabsf(f[i]), fabsf(f[i + 1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(f[i]));
+  }
+  return top;
+}
+
 template <int VEC>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* y, const E4m3Scale& scale) {
+__device__ __forceinline__ void store_codes(uint8_t* p, float* y, const E4m3Scale& scale) {
+  v_scale<VEC>(y, scale.a);
+  if (scale.twice) v_scale<VEC>(y, scale.b);
   if constexpr (VEC == 1) {
-    *p = static_cast<uint8_t>(e4m3_pair(scale(y[0]), 0.f) & 0xffu);
+    *p = static_cast<uint8_t>(e4m3_pair(y[0], 0.f) & 0xffu);
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i)
-      w[i] = e4m3_pair(scale(y[4 * i]), scale(y[4 * i + 1])) | (e4m3_pair(scale(y[4 * i + 2]), scale(y[4 * i + 3])) << 16);
+      w[i] = e4m3_pair(y[4 * i], y[4 * i + 1]) | (e4m3_pair(y[4 * i + 2], y[4 * i + 3]) << 16);
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   }
@@ -92,13 +166,13 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* y, const E4
 enum : int { kWeightNone = 0, kWeightF32 = 1, kWeightBf16 = 2 };
 
 // The weights of one chunk (16-byte aligned where VEC > 1, as the chunk is).
-template <int VEC, int WEIGHT>
-__device__ __forceinline__ void weights(const void* p, int col, float* w) {
-  if constexpr (WEIGHT == kWeightNone) {
+template <int VEC>
+__device__ __forceinline__ void weights(const NormArgs& a, int col, float* w) {
+  if (a.w_kind == kWeightNone) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) w[i] = 1.f;
-  } else if constexpr (WEIGHT == kWeightF32) {
-    const float* f = static_cast<const float*>(p) + col;
+  } else if (a.w_kind == kWeightF32) {
+    const float* f = static_cast<const float*>(a.w) + col;
     if constexpr (VEC == 1) {
       w[0] = f[0];
     } else {
@@ -112,7 +186,7 @@ __device__ __forceinline__ void weights(const void* p, int col, float* w) {
       }
     }
   } else {
-    const __nv_bfloat16* f = static_cast<const __nv_bfloat16*>(p) + col;
+    const __nv_bfloat16* f = static_cast<const __nv_bfloat16*>(a.w) + col;
     if constexpr (VEC == 8) {
       Chunk<__nv_bfloat16, 8> c;
       c.load(f);
@@ -129,23 +203,31 @@ __device__ __forceinline__ void weights(const void* p, int col, float* w) {
   }
 }
 
-// Sum (or maximum) over the TPR threads of a row: a part of a warp, or the whole CTA.
-template <int TPR, bool kMax>
-__device__ __forceinline__ float row_reduce(float v, float* smem) {
+// Sums (or maxima) of ROWS rows over the threads that hold them: TPR of a warp, or the whole CTA (TPR = 0)
+// through one barrier; callers alternate between the two buffers.
+template <int TPR, int ROWS, bool kMax>
+__device__ __forceinline__ void row_reduce(float (&v)[ROWS], float (*smem)[32], int& buf) {
 #pragma unroll
-  for (int off = (TPR < 32 ? TPR : 32) / 2; off > 0; off >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, v, off);
-    v = kMax ? fmaxf(v, o) : v + o;
-  }
-  if constexpr (TPR > 32) {
-    __syncthreads();  // the last reduction has been read
-    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  for (int off = (TPR == 0 ? 32 : TPR) / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float o = __shfl_xor_sync(0xffffffffu, v[r], off);
+      v[r] = kMax ? fmaxf(v[r], o) : v[r] + o;
+    }
+  if constexpr (TPR == 0) {
+    float (*mine)[32] = smem + buf * ROWS;
+    buf ^= 1;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) mine[r][threadIdx.x >> 5] = v[r];
     __syncthreads();
-    v = smem[0];
+    const int warps = blockDim.x >> 5;
 #pragma unroll
-    for (int w = 1; w < TPR / 32; ++w) v = kMax ? fmaxf(v, smem[w]) : v + smem[w];
+    for (int r = 0; r < ROWS; ++r) {
+      v[r] = mine[r][0];
+      for (int w = 1; w < warps; ++w) v[r] = kMax ? fmaxf(v[r], mine[r][w]) : v[r] + mine[r][w];
+    }
   }
-  return v;
 }
 
 __device__ __forceinline__ size_t row_at(const int64_t (&stride)[3], int b, int h, int n) {
@@ -156,12 +238,14 @@ __device__ __forceinline__ size_t row_at(const int64_t (&stride)[3], int b, int 
 // neighbouring rows of a [B, N, H, d] tensor.  Thread group g takes rows g, g + groups, ...
 // Rows and columns past the end load the last row or the first column again (every load is in bounds without a
 // branch) and count as zero.
-template <typename T, int VEC, int NV, int TPR, int ROWS, int CODES, int WEIGHT>
-__global__ void __launch_bounds__(CODES == kCodesBlock ? 1024 : 256) rms_norm_kernel(const NormArgs a) {
-  __shared__ float red[32];
+template <typename T, int VEC, int NV, int TPR, int ROWS, bool kBlock>
+__global__ void __launch_bounds__(kBlock ? 1024 : TPR != 0 ? 256 : 512) rms_norm_kernel(const NormArgs a) {
+  __shared__ float red[2 * ROWS][32];
+  int buf = 0;
   const int bh = static_cast<int>(blockIdx.x % a.BH), chunk = static_cast<int>(blockIdx.x / a.BH);
   const int b = bh / a.H, h = bh - b * a.H;
-  const int groups = blockDim.x / TPR, g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const int tpr = TPR == 0 ? blockDim.x : TPR, groups = TPR == 0 ? 1 : blockDim.x / TPR;
+  const int g = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int n0 = chunk * groups * ROWS + g;
   const T* x = static_cast<const T*>(a.x) + row_at(a.x_stride, b, h, 0);
   const bool has_res = a.res != nullptr;
@@ -174,256 +258,278 @@ __global__ void __launch_bounds__(CODES == kCodesBlock ? 1024 : 256) rms_norm_ke
     const int n = min(n0 + r * groups, a.N - 1);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = (j * TPR + t) * VEC;
+      const int col = (j * tpr + t) * VEC;
       cx[r][j].load(x + static_cast<size_t>(n) * a.x_stride[2] + (col < a.d ? col : 0));
     }
     if (has_res)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int col = (j * TPR + t) * VEC;
+        const int col = (j * tpr + t) * VEC;
         cr[r][j].load(res + static_cast<size_t>(n) * res_n + (col < a.d ? col : 0));
       }
   }
-  float s[ROWS][NV * VEC];
-  float amax = 0.f;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  float s[ROWS][NV * VEC], stat[ROWS], rstd[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const int n = n0 + r * groups;
-    float sq = 0.f;
+    stat[r] = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = (j * TPR + t) * VEC;
+      const int col = (j * tpr + t) * VEC;
       float* f = s[r] + j * VEC;
       cx[r][j].get(f);
       if (has_res) {
         float o[VEC];
         cr[r][j].get(o);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] += o[i];
+        v_add<VEC>(f, o);
         if (a.sum != nullptr && n < a.N && col < a.d)
           Chunk<T, VEC>::store(static_cast<T*>(a.sum) + (out_row + n) * a.d + col, f);
       }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (col >= a.d) f[i] = 0.f;
-        sq = fmaf(f[i], f[i], sq);
-      }
-    }
-    sq = row_reduce<TPR, false>(sq, red);
-    const float rstd = 1.f / sqrtf(sq / static_cast<float>(a.d) + a.eps);
-    if (t == 0 && n < a.N && a.rstd != nullptr) a.rstd[out_row + n] = rstd;
-    if (CODES == kCodesRow) amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = (j * TPR + t) * VEC;
-      float* f = s[r] + j * VEC;
-      float w[VEC];
-      weights<VEC, WEIGHT>(a.w, col < a.d ? col : 0, w);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        f[i] = col < a.d ? f[i] * rstd * w[i] : 0.f;
-        if (CODES != kCodesNone && n < a.N) amax = fmaxf(amax, fabsf(f[i]));
-      }
-      if (a.y != nullptr && n < a.N && col < a.d)
-        Chunk<T, VEC>::store(static_cast<T*>(a.y) + (out_row + n) * a.d + col, f);
-    }
-    if constexpr (CODES == kCodesRow) {
-      const int e = e4m3_block_exponent(fminf(row_reduce<TPR, true>(amax, red), FLT_MAX));
-      const E4m3Scale scale(e);
-      if (n < a.N) {
-        if (t == 0) a.exps[out_row + n] = e;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int col = (j * TPR + t) * VEC;
-          if (col < a.d) store_codes<VEC>(a.codes + (out_row + n) * a.d + col, s[r] + j * VEC, scale);
-        }
-      }
+      const float sq = v_dot<VEC>(f, f);
+      stat[r] += col < a.d ? sq : 0.f;
     }
   }
-  if constexpr (CODES == kCodesBlock) {  // the CTA's rows are the block
+  row_reduce<TPR, ROWS, false>(stat, red, buf);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) amax = fmaxf(amax, red[w]);
-    const int e = e4m3_block_exponent(fminf(amax, FLT_MAX));
-    const E4m3Scale scale(e);
-    if (threadIdx.x == 0) a.exps[static_cast<size_t>(bh) * a.chunks + chunk] = e;
+  for (int r = 0; r < ROWS; ++r) {
+    const int n = n0 + r * groups;
+    rstd[r] = rsqrtf(fmaf(stat[r], inv_d, a.eps));
+    if (t == 0 && n < a.N && a.rstd != nullptr) a.rstd[out_row + n] = rstd[r];
+    stat[r] = 0.f;  // from here the largest |y|
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = (j * tpr + t) * VEC;
+    float w[VEC];
+    weights<VEC>(a, col < a.d ? col : 0, w);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const int n = n0 + r * groups;
+      float* f = s[r] + j * VEC;
+      v_scale<VEC>(f, rstd[r]);
+      v_mul<VEC>(f, w);
+      if (kBlock || a.codes != nullptr) stat[r] = col < a.d ? v_top<VEC>(f, stat[r]) : stat[r];
+      if (a.y != nullptr && n < a.N && col < a.d)
+        Chunk<T, VEC>::store(static_cast<T*>(a.y) + (out_row + n) * a.d + col, f);
+    }
+  }
+  if (!kBlock && a.codes == nullptr) return;
+  int e[ROWS];
+  if constexpr (kBlock) {  // the CTA's rows are the block
+    float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int col = (j * TPR + t) * VEC;
-        if (n < a.N && col < a.d) store_codes<VEC>(a.codes + (out_row + n) * a.d + col, s[r] + j * VEC, scale);
-      }
+    for (int r = 0; r < ROWS; ++r)
+      if (n0 + r * groups < a.N) top = fmaxf(top, stat[r]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, red[0][w]);
+    const int be = e4m3_block_exponent(fminf(top, FLT_MAX));
+    if (threadIdx.x == 0) a.exps[static_cast<size_t>(bh) * a.chunks + chunk] = be;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) e[r] = be;
+  } else {
+    row_reduce<TPR, ROWS, true>(stat, red, buf);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int n = n0 + r * groups;
+      e[r] = e4m3_block_exponent(fminf(stat[r], FLT_MAX));
+      if (t == 0 && n < a.N) a.exps[out_row + n] = e[r];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int n = n0 + r * groups;
+    const E4m3Scale scale(e[r]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = (j * tpr + t) * VEC;
+      if (n < a.N && col < a.d) store_codes<VEC>(a.codes + (out_row + n) * a.d + col, s[r] + j * VEC, scale);
     }
   }
 }
 
-// Persistent CTAs walk the chunks; every thread keeps the dw of its columns in fp32 and the CTA's sum goes to
-// one row of the workspace, which rms_norm_dw_kernel adds up in a fixed order (no atomics).
-template <typename T, int VEC, int NV, int TPR, int ROWS, int WEIGHT>
-__global__ void __launch_bounds__(256) rms_norm_bwd_kernel(const NormBwdArgs a) {
+// Persistent CTAs walk the chunks; every thread keeps the weights and the dw of its columns in registers, and the
+// CTA's sum goes to one row of the workspace, which rms_norm_dw_kernel adds up in a fixed order (no atomics).
+template <typename T, int VEC, int NV, int TPR, int ROWS>
+__global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 && NV == 4 ? 1024 : 512, TPR != 0 ? 2 : 1)
+    rms_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int C = NV * VEC;
-  extern __shared__ float dw_smem[];  // d floats (TPR <= 32)
-  __shared__ float red[32];
-  constexpr int groups = 256 / TPR;
-  const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
-  float dw[C];
+  __shared__ float red[2 * ROWS][32];
+  __shared__ float dw_smem[TPR == 0 ? 1 : C * TPR];
+  int buf = 0;
+  const int tpr = TPR == 0 ? blockDim.x : TPR, groups = TPR == 0 ? 1 : blockDim.x / TPR;
+  const int g = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int d = a.n.d, N = a.n.N;
+  // the weights stay in registers where there is room; elsewhere each row reads them again (from L1)
+  constexpr bool kHoldW = C <= 16;
+  float w[kHoldW ? C : 1], dw[C];
 #pragma unroll
-  for (int i = 0; i < C; ++i) dw[i] = 0.f;
-  const float inv_d = 1.f / static_cast<float>(a.n.d);
+  for (int j = 0; j < NV; ++j) {
+    const int col = (j * tpr + t) * VEC;
+    if constexpr (kHoldW) weights<VEC>(a.n, col < d ? col : 0, w + j * VEC);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) dw[j * VEC + i] = 0.f;
+  }
+  const float inv_d = 1.f / static_cast<float>(d);
+  const bool has_ds = a.d_sum != nullptr;
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* ds = has_ds ? static_cast<const T*>(a.d_sum) : dy;
   const long long items = static_cast<long long>(a.n.chunks) * a.n.BH;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int bh = static_cast<int>(item % a.n.BH), chunk = static_cast<int>(item / a.n.BH);
     const int b = bh / a.n.H, h = bh - b * a.n.H;
     const int n0 = chunk * groups * ROWS + g;
-    const size_t out_row = static_cast<size_t>(bh) * a.n.N;
+    const size_t out_row = static_cast<size_t>(bh) * N;
     const T* s = static_cast<const T*>(a.n.x) + row_at(a.n.x_stride, b, h, 0);
     T* dx = static_cast<T*>(a.dx) + row_at(a.n.res_stride, b, h, 0);
-    const T* dy = static_cast<const T*>(a.dy);
-    const bool has_ds = a.d_sum != nullptr;
-    const T* ds = has_ds ? static_cast<const T*>(a.d_sum) : dy;
-    Chunk<T, VEC> cs[ROWS][NV], cy[ROWS][NV];
-    float rstd[ROWS];
+    Chunk<T, VEC> cs[ROWS][NV], cy[ROWS][NV], cd[ROWS][NV];
+    float rstd[ROWS], dot[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const int n = min(n0 + r * groups, a.n.N - 1);
+      const int n = min(n0 + r * groups, N - 1);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int col = (j * TPR + t) * VEC, at = col < a.n.d ? col : 0;
+        const int col = (j * tpr + t) * VEC, at = col < d ? col : 0;
         cs[r][j].load(s + static_cast<size_t>(n) * a.n.x_stride[2] + at);
-        cy[r][j].load(dy + (out_row + n) * a.n.d + at);
+        cy[r][j].load(dy + (out_row + n) * d + at);
+        if (has_ds) cd[r][j].load(ds + (out_row + n) * d + at);
       }
       rstd[r] = a.n.rstd[out_row + n];
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
+      const bool in = n0 + r * groups < N;
+      dot[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int col = (j * tpr + t) * VEC;
+        float xh[VEC], fy[VEC], wt[VEC];
+        cs[r][j].get(xh);
+        cy[r][j].get(fy);
+        if constexpr (!kHoldW) weights<VEC>(a.n, col < d ? col : 0, wt);
+        v_scale<VEC>(xh, rstd[r]);
+        if (in) v_fma<VEC>(dw + j * VEC, fy, xh);
+        v_mul<VEC>(fy, kHoldW ? w + j * VEC : wt);
+        const float p = v_dot<VEC>(fy, xh);
+        dot[r] += col < d ? p : 0.f;
+      }
+    }
+    row_reduce<TPR, ROWS, false>(dot, red, buf);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
       const int n = n0 + r * groups;
-      Chunk<T, VEC> cd[NV];
-      const bool in = n < a.n.N;
-      if (has_ds) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int col = (j * TPR + t) * VEC;
-          cd[j].load(ds + (out_row + min(n, a.n.N - 1)) * a.n.d + (col < a.n.d ? col : 0));
-        }
-      }
-      float dot = 0.f;
+      // dx = rstd * (dy * w) - (rstd^2 * mean) * s
+      const float c = -rstd[r] * rstd[r] * dot[r] * inv_d;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int col = (j * TPR + t) * VEC;
-        float fs[VEC], fy[VEC], w[VEC];
+        const int col = (j * tpr + t) * VEC;
+        float fs[VEC], fy[VEC], out[VEC], wt[VEC];
         cs[r][j].get(fs);
         cy[r][j].get(fy);
-        weights<VEC, WEIGHT>(a.n.w, col < a.n.d ? col : 0, w);
+        if constexpr (!kHoldW) weights<VEC>(a.n, col < d ? col : 0, wt);
+        if (has_ds) {
+          cd[r][j].get(out);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float xh = fs[i] * rstd[r];
-          if (in) dw[j * VEC + i] = fmaf(fy[i], xh, dw[j * VEC + i]);
-          if (col < a.n.d) dot = fmaf(fy[i] * w[i], xh, dot);
+          for (int i = 0; i < VEC; ++i) out[i] = 0.f;
         }
-      }
-      dot = row_reduce<TPR, false>(dot, red) * inv_d;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int col = (j * TPR + t) * VEC;
-        if (!in || col >= a.n.d) continue;
-        float fs[VEC], fy[VEC], w[VEC], fd[VEC], out[VEC];
-        cs[r][j].get(fs);
-        cy[r][j].get(fy);
-        weights<VEC, WEIGHT>(a.n.w, col, w);
-        if (has_ds) cd[j].get(fd);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          out[i] = rstd[r] * (fy[i] * w[i] - fs[i] * rstd[r] * dot);
-          if (has_ds) out[i] += fd[i];
-        }
-        Chunk<T, VEC>::store(dx + static_cast<size_t>(n) * a.n.res_stride[2] + col, out);
+        v_scale<VEC>(fs, c);
+        v_add<VEC>(out, fs);
+        v_scale<VEC>(fy, rstd[r]);
+        v_fma<VEC>(out, fy, kHoldW ? w + j * VEC : wt);
+        if (n < N && col < d) Chunk<T, VEC>::store(dx + static_cast<size_t>(n) * a.n.res_stride[2] + col, out);
       }
     }
   }
   if (a.partial == nullptr) return;
-  float* mine = a.partial + static_cast<size_t>(blockIdx.x) * a.n.d;
-  if constexpr (TPR > 32) {
+  float* mine = a.partial + static_cast<size_t>(blockIdx.x) * d;
+  if constexpr (TPR == 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const int col = (j * TPR + t) * VEC + i;
-        if (col < a.n.d) mine[col] = dw[j * VEC + i];
+        const int col = (j * tpr + t) * VEC + i;
+        if (col < d) mine[col] = dw[j * VEC + i];
       }
   } else {
 #pragma unroll
     for (int off = 16; off >= TPR; off >>= 1)
 #pragma unroll
       for (int i = 0; i < C; ++i) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], off);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int w = 0; w < 8; ++w) {
-      if (warp == w && lane < TPR) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int k = 0; k < warps; ++k) {
+      if (warp == k && lane < TPR) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             const int col = (j * TPR + t) * VEC + i;
-            if (col < a.n.d) dw_smem[col] = w == 0 ? dw[j * VEC + i] : dw_smem[col] + dw[j * VEC + i];
+            dw_smem[col] = k == 0 ? dw[j * VEC + i] : dw_smem[col] + dw[j * VEC + i];
           }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.n.d; c += 256) mine[c] = dw_smem[c];
+    for (int c = threadIdx.x; c < d; c += blockDim.x) mine[c] = dw_smem[c];
   }
 }
 
-// dw[c] = sum of the CTAs' rows, in fp64 (a few hundred terms): 8 threads a column, each a fixed share.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* __restrict__ partial, int rows, int d,
-                                                          float* __restrict__ dw) {
-  __shared__ double part[8][32];
+// dw[c] = sum of the CTAs' rows, in fp64 (some hundred terms): 32 threads a column, each a fixed share.
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restrict__ partial, int rows, int d,
+                                                           float* __restrict__ dw) {
+  __shared__ double part[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
   double s = 0.0;
-  if (c < d)
-    for (int r = k; r < rows; r += 8) s += static_cast<double>(partial[static_cast<size_t>(r) * d + c]);
+  const int cc = min(c, d - 1);
+#pragma unroll 4
+  for (int r = k; r < rows; r += 32) s += static_cast<double>(partial[static_cast<size_t>(r) * d + cc]);
   part[k][threadIdx.x & 31] = s;
   __syncthreads();
-  if (k == 0 && c < d) {
-    for (int j = 1; j < 8; ++j) s += part[j][threadIdx.x];
-    dw[c] = static_cast<float>(s);
-  }
+  // warp k adds up column k
+  s = part[threadIdx.x & 31][k];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + k < d) dw[blockIdx.x * 32 + k] = static_cast<float>(s);
 }
 
-// How a row of d elements is held: VEC elements a load, NV loads a thread, TPR threads a row, ROWS rows at a
-// time.  with_hold calls f with the smallest that holds it.
+// How a row of d elements is held: VEC elements a load, NV loads a thread, TPR threads of a warp (0: a whole CTA
+// of as many threads as the row needs), ROWS rows at a time.
 template <int V, int N, int P, int R>
 struct Hold {
   static constexpr int VEC = V, NV = N, TPR = P, ROWS = R;
+  // threads of a CTA for n loads a row
+  static int threads(int n) { return P != 0 ? 256 : (n + N * 32 - 1) / (N * 32) * 32; }
 };
 
-template <typename T, typename F>
+// Calls f with the Hold of a forward (or gradient) row and its number of loads.  A row stays in a warp, without
+// a barrier, while the warp's registers hold it: up to 256 loads forward; the gradient, which holds up to three
+// rows and the sums of its columns, up to 128, then takes 64 threads and more.
+template <typename T, bool kBwd, typename F>
 cudaError_t with_hold(int d, bool vectors, F&& f) {
   constexpr int V = 16 / sizeof(T);
   const int n = vectors ? d / V : d;  // loads a row
   if (vectors) {
-    if (n <= 8) return f(Hold<V, 1, 8, 4>());
-    if (n <= 16) return f(Hold<V, 1, 16, 4>());
-    if (n <= 32) return f(Hold<V, 1, 32, 4>());
-    if (n <= 64) return f(Hold<V, 2, 32, 2>());
-    if (n <= 128) return f(Hold<V, 4, 32, 1>());
-    if (n <= 192) return f(Hold<V, 6, 32, 1>());
-    if (n <= 256) return f(Hold<V, 8, 32, 1>());
-    if (n <= 512) return f(Hold<V, 2, 256, 1>());
-    if (n <= 1024) return f(Hold<V, 4, 256, 1>());
-    if (n <= 2048) return f(Hold<V, 8, 256, 1>());
-    if constexpr (V == 4)
-      if (n <= 4096) return f(Hold<V, 16, 256, 1>());
-  } else {
-    if (n <= 32) return f(Hold<1, 1, 32, 4>());
-    if (n <= 128) return f(Hold<1, 4, 32, 4>());
-    if (n <= 512) return f(Hold<1, 16, 32, 1>());
-    if (n <= 4096) return f(Hold<1, 16, 256, 1>());
-    if (n <= 16384) return f(Hold<1, 64, 256, 1>());
+    if (n <= 8) return f(Hold<V, 2, 4, 2>(), n);
+    if (n <= 16) return f(Hold<V, 2, 8, 2>(), n);
+    if (n <= 32) return f(Hold<V, 2, 16, 2>(), n);
+    if (n <= 64) return f(Hold<V, 2, 32, 2>(), n);
+    if (n <= 128) return f(Hold<V, 4, 32, 1>(), n);
+    if constexpr (kBwd) {
+      if (n <= 192) return f(Hold<V, 3, 0, 1>(), n);
+      return f(Hold<V, 4, 0, 1>(), n);
+    } else {
+      if (n <= 192) return f(Hold<V, 6, 32, 1>(), n);
+      if (n <= 256) return f(Hold<V, 8, 32, 1>(), n);
+      if (n <= 1024) return f(Hold<V, 4, 0, 1>(), n);
+      return f(Hold<V, 8, 0, 1>(), n);
+    }
   }
-  return cudaErrorInvalidValue;
+  if (n <= 32) return f(Hold<1, 1, 32, 4>(), n);
+  if (n <= 128) return f(Hold<1, 4, 32, 4>(), n);
+  if (n <= 4096) return f(Hold<1, 8, 0, 1>(), n);
+  return f(Hold<1, 32, 0, 1>(), n);
 }
 
 // Whether every row starts on 16 bytes and is a whole number of 16-byte loads.
@@ -435,46 +541,47 @@ bool vector_rows(const NormArgs& a, int es) {
   return ok;
 }
 
-template <typename T, int WEIGHT>
+template <typename T>
 cudaError_t launch_norm_t(NormArgs a, cudaStream_t stream) {
-  return with_hold<T>(a.d, vector_rows(a, sizeof(T)), [&](auto hold) -> cudaError_t {
+  return with_hold<T, false>(a.d, vector_rows(a, sizeof(T)), [&](auto hold, int n) -> cudaError_t {
     using H = decltype(hold);
     const bool blocks = a.codes != nullptr && a.block > 1;
-    const int threads = blocks ? a.block * H::TPR / H::ROWS : 256;
-    const int rows = threads / H::TPR * H::ROWS;
+    const int threads = blocks ? a.block * H::TPR / H::ROWS : H::threads(n);
+    const int rows = (H::TPR == 0 ? 1 : threads / H::TPR) * H::ROWS;
     a.chunks = static_cast<int>((static_cast<long long>(a.N) + rows - 1) / rows);
     const long long grid = static_cast<long long>(a.chunks) * a.BH;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const unsigned gr = static_cast<unsigned>(grid);
-    if (blocks) {
-      if constexpr (H::TPR <= 32 && H::NV <= 4) {  // rows of 64 or 128
-        rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kCodesBlock, WEIGHT><<<gr, threads, 0, stream>>>(a);
-        return cudaGetLastError();
-      }
-      return cudaErrorInvalidValue;
+    if (!blocks) {
+      rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, false><<<gr, threads, 0, stream>>>(a);
+      return cudaGetLastError();
     }
-    if (a.codes != nullptr)
-      rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kCodesRow, WEIGHT><<<gr, threads, 0, stream>>>(a);
-    else
-      rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kCodesNone, WEIGHT><<<gr, threads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if constexpr (H::TPR != 0 && (H::NV <= 2 || H::VEC == 1)) {  // rows of 64 or 128
+      rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, true><<<gr, threads, 0, stream>>>(a);
+      return cudaGetLastError();
+    }
+    return cudaErrorInvalidValue;
   });
 }
 
-template <typename T, int WEIGHT>
+// CTAs of the gradient: as many as 148 SMs hold at up to 128 registers a thread.
+template <typename H>
+int bwd_ctas(int n) {
+  return 148 * (H::threads(n) < 512 ? 512 / H::threads(n) : 1);
+}
+
+template <typename T>
 cudaError_t launch_norm_bwd_t(NormBwdArgs a, float* dw, cudaStream_t stream) {
-  return with_hold<T>(a.n.d, vector_rows(a.n, sizeof(T)), [&](auto hold) -> cudaError_t {
+  return with_hold<T, true>(a.n.d, vector_rows(a.n, sizeof(T)), [&](auto hold, int n) -> cudaError_t {
     using H = decltype(hold);
-    constexpr int ROWS = H::ROWS > 2 ? 2 : H::ROWS;
-    const int rows = 256 / H::TPR * ROWS;
+    const int threads = H::threads(n), rows = (H::TPR == 0 ? 1 : threads / H::TPR) * H::ROWS;
     a.n.chunks = static_cast<int>((static_cast<long long>(a.n.N) + rows - 1) / rows);
     const long long items = static_cast<long long>(a.n.chunks) * a.n.BH;
-    const int grid = static_cast<int>(items < kNormBwdCtas ? items : kNormBwdCtas);
-    const int smem = H::TPR <= 32 ? a.n.d * 4 : 0;
-    rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, ROWS, WEIGHT><<<grid, 256, smem, stream>>>(a);
+    const int most = bwd_ctas<H>(n), grid = static_cast<int>(items < most ? items : most);
+    rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS><<<grid, threads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || dw == nullptr) return e;
-    rms_norm_dw_kernel<<<(a.n.d + 31) / 32, 256, 0, stream>>>(a.partial, grid, a.n.d, dw);
+    rms_norm_dw_kernel<<<(a.n.d + 31) / 32, 1024, 0, stream>>>(a.partial, grid, a.n.d, dw);
     return cudaGetLastError();
   });
 }
@@ -494,28 +601,32 @@ void collapse(NormArgs* a) {
 
 }  // namespace
 
+size_t rms_norm_bwd_partials(long long rows, int d, bool f32) {
+  // whether the rows are read as vectors shows only with the pointers: the larger of the two
+  long long most = 0;
+  for (const bool vectors : {false, true}) {
+    if (vectors && d % (f32 ? 4 : 8) != 0) continue;
+    auto count = [&](auto hold, int n) {
+      const long long c = bwd_ctas<decltype(hold)>(n);
+      most = c > most ? c : most;
+      return cudaSuccess;
+    };
+    f32 ? with_hold<float, true>(d, vectors, count) : with_hold<__nv_bfloat16, true>(d, vectors, count);
+  }
+  return static_cast<size_t>(rows < most ? rows : most);
+}
+
 cudaError_t launch_rms_norm(NormArgs a, bool f32, cudaStream_t stream) {
   if (a.codes == nullptr) a.block = 1;
   collapse(&a);
-  if (a.w == nullptr)
-    return f32 ? launch_norm_t<float, kWeightNone>(a, stream) : launch_norm_t<__nv_bfloat16, kWeightNone>(a, stream);
-  if (a.w_f32)
-    return f32 ? launch_norm_t<float, kWeightF32>(a, stream) : launch_norm_t<__nv_bfloat16, kWeightF32>(a, stream);
-  return f32 ? launch_norm_t<float, kWeightBf16>(a, stream) : launch_norm_t<__nv_bfloat16, kWeightBf16>(a, stream);
+  return f32 ? launch_norm_t<float>(a, stream) : launch_norm_t<__nv_bfloat16>(a, stream);
 }
 
 cudaError_t launch_rms_norm_bwd(NormBwdArgs a, bool f32, float* dw, cudaStream_t stream) {
   a.n.block = 1;
   a.n.res = a.dx;  // its strides and alignment count as the residual's do
   collapse(&a.n);
-  if (a.n.w == nullptr)
-    return f32 ? launch_norm_bwd_t<float, kWeightNone>(a, dw, stream)
-               : launch_norm_bwd_t<__nv_bfloat16, kWeightNone>(a, dw, stream);
-  if (a.n.w_f32)
-    return f32 ? launch_norm_bwd_t<float, kWeightF32>(a, dw, stream)
-               : launch_norm_bwd_t<__nv_bfloat16, kWeightF32>(a, dw, stream);
-  return f32 ? launch_norm_bwd_t<float, kWeightBf16>(a, dw, stream)
-             : launch_norm_bwd_t<__nv_bfloat16, kWeightBf16>(a, dw, stream);
+  return f32 ? launch_norm_bwd_t<float>(a, dw, stream) : launch_norm_bwd_t<__nv_bfloat16>(a, dw, stream);
 }
 
 }  // namespace vsa

@@ -471,9 +471,9 @@ VSA_API vsa_status vsa_rms_norm(const void *x, const void *residual, vsa_dtype d
                                 vsa_dtype weight_dtype, const vsa_norm_shape *shape, void *sum, void *y,
                                 uint8_t *codes, int32_t *d_exp, float *rstd, cudaStream_t stream);
 
-/* Workspace bytes of vsa_rms_norm_bwd with d_weight (up to 592 partial sums of d fp32); 0 for an
- * invalid shape. */
-VSA_API size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape *shape);
+/* Workspace bytes of vsa_rms_norm_bwd with d_weight (the partial sums of its CTAs, d fp32 each); 0 for
+ * an invalid shape. */
+VSA_API size_t vsa_rms_norm_bwd_workspace_size(const vsa_norm_shape *shape, vsa_dtype dtype);
 
 /*
  * Gradient of vsa_rms_norm: with xh = s * rstd and g = dy * weight,

@@ -112,7 +112,7 @@ def test_norm_refused_before_launch():
     for bad in (dict(B=0), dict(H=-1), dict(N=0), dict(d=0), dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")),
                 dict(x_stride=(1, -1, 1)), dict(res_stride=(1 << 50, 1, 1))):
         assert fwd(**bad) == inv and bwd(**bad) == inv
-        assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(**{**good, **bad})) == 0
+        assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(**{**good, **bad}), 1) == 0
     for bad in (dict(d=16385), dict(B=1 << 20, H=1 << 20), dict(B=1 << 10, H=1 << 10, N=1 << 12)):
         assert fwd(**bad) == uns and bwd(**bad) == uns
     assert fwd(x=None) == inv and fwd(x=FAKE + 1) == inv and fwd(dtype=2) == inv and fwd(wt=5) == inv
@@ -129,5 +129,9 @@ def test_norm_refused_before_launch():
     assert bwd(ws=None) == inv and bwd(wsb=8) == _lib.VSA_ERR_WORKSPACE
     assert bwd(res_stride=(0, 64, 32)) == inv                       # rows of dx that overlap
     assert bwd(res_stride=(0, 0, 64)) == inv                        # heads of dx that coincide
-    assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(**good)) == 20 * 64 * 4
-    assert _lib.vsa_rms_norm_bwd_workspace_size(_lib.make_norm_shape(1, 1, 10000, 100)) == -(-592 * 100 * 4 // 256) * 256
+    size = _lib.vsa_rms_norm_bwd_workspace_size
+    assert size(_lib.make_norm_shape(**good), 1) == 20 * 64 * 4          # a row of partial sums for each row at most
+    assert size(_lib.make_norm_shape(**good), 2) == 0
+    for d in (1, 64, 100, 1536, 16384):                                  # and at most a few MB a kernel's width
+        for dtype in (0, 1):
+            assert 4 * d <= size(_lib.make_norm_shape(1, 1, 1 << 20, d), dtype) <= 148 * 512 * 32 * 4 + 256
