@@ -92,13 +92,26 @@ class _HostPipelined:
 
 
 
+_HERE = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _there(stream, device):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(int(stream), device=device)):
+                yield
+
+
 def _on(stream, device):
-    """Context in which `stream` (a torch stream or a raw handle; None: the current one) is current, so that
-    what is allocated in it belongs to the stream that uses it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream), device=device))
+    """Context in which `device` and `stream` (a torch stream or a raw handle; None: the device's current one)
+    are current, so that what is allocated in it belongs to the stream that uses it."""
+    if stream is None and (device.type != "cuda" or device.index == torch.cuda.current_device()):
+        return _HERE
+    return _there(stream, device)
 
 
 def _no_capture(what: str):
@@ -113,7 +126,7 @@ class _Attend(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, q, k, v, kinds):
         ctx.set_materialize_grads(False)
-        with torch.cuda.device(plan.device):
+        with _on(None, plan.device):
             o, lse = plan(q, k, v, kinds=kinds)
             ctx.plan = plan
             ctx.save_for_backward(q, k, v, o, lse, plan.kinds.clone())
@@ -226,7 +239,7 @@ class SparseAttention(_HostPipelined):
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
         shape = (self.B, self.H, self.N, self.d)
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with _on(stream, self.device):
             if out is None:
                 out = tuple(torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(3))
             if len(out) != 3:
@@ -411,15 +424,18 @@ class RMSNorm:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.B, self.H, self.N, self.d, self.dtype, self.device = B, H, N, d, dtype, dev
-        self.eps, self.quantize, self.keep_y, self.with_grad = eps, quantize, keep_y or not quantize, with_grad
-        need = vsa_rms_norm_bwd_workspace_size(self._shape(), _DTYPE[dtype])
+        self.quantize, self.keep_y, self.with_grad = quantize, keep_y or not quantize, with_grad
+        self.shape = make_norm_shape(B, H, N, d, block=max(quantize, 1), eps=eps)
+        need = vsa_rms_norm_bwd_workspace_size(self.shape, _DTYPE[dtype])
         if need == 0:
             raise VsaError(_lib.VSA_ERR_INVALID_ARG, "vsa_rms_norm_bwd_workspace_size")
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev) if with_grad else None
 
     def _shape(self, x=None, residual=None):
-        strides = [(0, 0, 0) if t is None or t.is_contiguous() else t.stride()[:3] for t in (x, residual)]
-        return make_norm_shape(self.B, self.H, self.N, self.d, *strides, block=max(self.quantize, 1), eps=self.eps)
+        strides = tuple((0, 0, 0) if t is None or t.is_contiguous() else t.stride()[:3] for t in (x, residual))
+        if strides == ((0, 0, 0), (0, 0, 0)):
+            return self.shape
+        return make_norm_shape(self.B, self.H, self.N, self.d, *strides, block=self.shape.block, eps=self.shape.eps)
 
     def _rows(self, t: torch.Tensor, what: str, dense: bool = False) -> torch.Tensor:
         shape = (self.B, self.H, self.N, self.d)
@@ -442,7 +458,7 @@ class RMSNorm:
                  stream=None) -> NormOut:
         wt = self._weight(weight)
         shape = (self.B, self.H, self.N, self.d)
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with _on(stream, self.device):
             x = self._rows(x, "x")
             residual = None if residual is None else self._rows(residual, "the residual")
             new = lambda *sh, dtype: torch.empty(*sh, dtype=dtype, device=self.device)  # noqa: E731
@@ -463,7 +479,7 @@ class RMSNorm:
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
         wt = self._weight(weight)
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with _on(stream, self.device):
             dy = self._rows(dy, "dy", dense=True)
             d_sum = None if d_sum is None else self._rows(d_sum, "d_sum", dense=True)
             s = self._rows(s, "s")
