@@ -182,6 +182,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
 
   if (kind > kCube || (kind == kCube && g.ncubes == 0)) {
     // unknown layout: this block's rows of the natural-order gradients become zeros
+    pdl_wait();
     if (tid == 0 && blk == 0) atomicOr(a.err, kDevErrKind);
     const int r0 = blk * BN, r1 = min(r0 + BN, a.nat_rows);
     for (int x = tid; x < (r1 - r0) * (D / 8); x += kBwdThreads) {
@@ -197,7 +198,10 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
   }
   const int rows = layout_rows(g, kind);
   const int nb_head = (rows + BN - 1) / BN;
-  if (blk >= nb_head) return;
+  if (blk >= nb_head) {
+    pdl_wait();  // no CTA ends before the kernel in front has
+    return;
+  }
   const BwdMaps* m = a.has_perm && kind != kSpatial ? mp : mn;
 
   // ---- barriers, the resident tiles, the blocks this CTA walks, TMEM ----
@@ -239,6 +243,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
     tmem_alloc(sbase + rest + C::OFF_MISC, C::TM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();  // from here the bitsets and the rows' terms
   const uint32_t* rbits = a.rbits + static_cast<size_t>(bh) * g.nblk * nwords;
   if (kKey) {
     for (int w = warp; w < nwords; w += kSoftmaxWarps) {
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------------------
 // Row terms and row bitsets
 // ---------------------------------------------------------------------------------------
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256, kPrepRows = 2;
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -599,17 +604,19 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
 
 // Eight values of a row as bf16 (fp32 rows round to nearest even, as the permuted copies do).
 __device__ __forceinline__ uint4 load8(const void* p, size_t at, bool f32) {
-  if (!f32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+  if (!f32) return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
   const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-  const float4 a = __ldg(q), b = __ldg(q + 1);
+  const float4 a = q[0], b = q[1];
   return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
 }
 
 // CTAs [0, mask_ctas): one warp per query block checks its list (ascending, in range, count within
 // max_kv) and writes it as bits; a bad list sets the error bit and becomes empty.
-// The others: d / 8 threads per slot of a head's padded rows; the two terms of the slot's row.
+// The others: d / 16 threads per slot of a head's padded rows, kPrepRows slots at a time so that every thread has
+// eight 16-byte loads in flight; the two terms of each slot's row.
 __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a) {
   const Geom& g = a.g;
+  pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) < a.mask_ctas) {
     const int nwords = (g.nblk + 31) >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -644,36 +651,51 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
     }
     return;
   }
-  const int tpr = a.d / 8;
+  const int tpr = a.d / 16, groups = kPrepThreads / tpr;
   const int slots = g.nblk * g.block;
-  const long long at = static_cast<long long>(blockIdx.x - a.mask_ctas) * (kPrepThreads / tpr) + threadIdx.x / tpr;
+  const long long first = static_cast<long long>(blockIdx.x - a.mask_ctas) * (groups * kPrepRows) + threadIdx.x / tpr;
+  const long long all = static_cast<long long>(a.BH) * slots;
   const int c = threadIdx.x % tpr;
-  const bool in = at < static_cast<long long>(a.BH) * slots;
-  const int bh = in ? static_cast<int>(at / slots) : 0, slot = in ? static_cast<int>(at - static_cast<long long>(bh) * slots) : 0;
-  const int kind = a.kinds[bh];
-  int token = in && kind <= kCube ? token_of_slot(g, kind, slot) : -1;
-  float delta = 0.f, lse = -INFINITY;
-  if (token >= 0) {
-    // whole call: O, dO and LSE in natural order; lists: each head's own layout and set
+  uint4 o[kPrepRows][2], go[kPrepRows][2];
+  float lse[kPrepRows], dlse[kPrepRows];
+  bool has[kPrepRows];
+#pragma unroll
+  for (int r = 0; r < kPrepRows; ++r) {
+    const long long at = min(first + r * groups, all - 1);
+    const int bh = static_cast<int>(at / slots), slot = static_cast<int>(at - static_cast<long long>(bh) * slots);
+    const int kind = a.kinds[bh];
+    const int token = kind <= kCube && !(kind == kCube && g.ncubes == 0) ? token_of_slot(g, kind, slot) : -1;
+    has[r] = token >= 0;
+    // whole call: O, dO and LSE in natural order; lists: each head's own layout and set.  A slot without a
+    // token loads row 0 of its head.
     const bool perm = !a.by_token && a.has_perm && kind != kSpatial;
-    const int r = a.by_token ? token : slot;
     const int stride = a.by_token ? g.N : (perm ? g.R : a.nat_rows);
-    const size_t rowi = static_cast<size_t>(bh) * stride + r;
-    const void* o = perm ? a.o_perm : a.o_nat;
-    const void* go = perm ? a.do_perm : a.do_nat;
+    const size_t row = static_cast<size_t>(bh) * stride + (has[r] ? (a.by_token ? token : slot) : 0);
+    const void* po = perm ? a.o_perm : a.o_nat;
+    const void* pg = perm ? a.do_perm : a.do_nat;
     const float* dl = perm ? a.dlse_perm : a.dlse_nat;
-    delta = dot8(load8(o, rowi * a.d + c * 8, a.f32), load8(go, rowi * a.d + c * 8, a.f32));
-    lse = (perm ? a.lse_perm : a.lse_nat)[rowi];
-    if (c == 0 && dl != nullptr) delta -= dl[rowi];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      o[r][j] = load8(po, row * a.d + (j * tpr + c) * 8, a.f32);
+      go[r][j] = load8(pg, row * a.d + (j * tpr + c) * 8, a.f32);
+    }
+    lse[r] = (perm ? a.lse_perm : a.lse_nat)[row];
+    dlse[r] = 0.f;
+    if (dl != nullptr) dlse[r] = dl[row];
   }
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1)
-    if (off < tpr) delta += __shfl_xor_sync(0xffffffffu, delta, off);
-  if (in && c == 0) {
-    const bool sees = lse != -INFINITY;
-    float* t = a.terms + (static_cast<size_t>(bh) * g.nblk + slot / g.block) * (2 * g.block) + slot % g.block;
-    t[0] = sees ? -lse * 1.4426950408889634f : -INFINITY;
-    t[g.block] = sees ? -delta : 0.f;
+  for (int r = 0; r < kPrepRows; ++r) {
+    float delta = dot8(o[r][0], go[r][0]) + dot8(o[r][1], go[r][1]);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1)
+      if (off < tpr) delta += __shfl_xor_sync(0xffffffffu, delta, off);
+    const long long at = first + r * groups;
+    if (c == 0 && at < all) {
+      const bool sees = has[r] && lse[r] != -INFINITY;
+      float* t = a.terms + (at / g.block) * (2 * g.block) + at % g.block;  // slots are whole blocks
+      t[0] = sees ? -lse[r] * 1.4426950408889634f : -INFINITY;
+      t[g.block] = sees ? dlse[r] - delta : 0.f;
+    }
   }
 }
 
@@ -687,8 +709,20 @@ cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cud
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(2 * a.BH * a.g.nblk), kBwdThreads, smem, stream>>>(nat, perm, a);
-  return cudaGetLastError();
+  // may start while the last prep CTAs still run (programmatic dependent launch): everything up to
+  // pdl_wait() in the kernel needs only what was there before prep
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * a.BH * a.g.nblk));
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, nat, perm, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -703,7 +737,7 @@ cudaError_t launch_sparse_attn_bwd(const BwdMaps& nat, const BwdMaps& perm, BwdP
                                    cudaStream_t stream) {
   const long long lists = static_cast<long long>(a.BH) * a.g.nblk;
   const long long slots = lists * a.g.block;
-  const int rows_per_cta = kPrepThreads / (d / 8);
+  const int rows_per_cta = kPrepThreads / (d / 16) * kPrepRows;
   prep.mask_ctas = static_cast<int>((lists + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
   const long long grid = prep.mask_ctas + (slots + rows_per_cta - 1) / rows_per_cta;
   bwd_prep_kernel<<<static_cast<unsigned>(grid), kPrepThreads, 0, stream>>>(prep);

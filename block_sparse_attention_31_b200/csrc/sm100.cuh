@@ -331,6 +331,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
       : "memory");
 }
 
+// Programmatic dependent launch: the kernel behind this one in the stream may be scheduled from here on; and that
+// kernel's wait until this one has completed and its writes are visible.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // True in one lane of a converged warp.  The assembler knows that a branch on it leaves a single thread.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
