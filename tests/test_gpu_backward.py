@@ -298,6 +298,112 @@ def test_on_another_stream():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d,block", [(128, 128), (64, 64)])
+def test_very_long_head(d, block):
+    """So many blocks that the bitset takes a ring stage's place; a few blocks a list, near and far."""
+    nb = 5700
+    N = nb * block - 13
+    shape = _lib.make_shape(1, 1, 1, 1, N, d, block)
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, v, do = (torch.randn(1, 1, N, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(4))
+    i = torch.arange(nb, device="cuda")
+    idx = torch.stack([i, (i * 7 + 3) % nb, (nb - 1 - i)], 1).sort(1).values
+    dup = torch.cat([torch.zeros(nb, 1, dtype=torch.bool, device="cuda"), idx[:, 1:] == idx[:, :-1]], 1)
+    idx = torch.where(dup, nb + 1, idx).sort(1).values
+    cnt = (idx < nb).sum(1).to(torch.int32).contiguous()
+    idx = torch.where(idx < nb, idx, -1).to(torch.int32).contiguous()
+    kinds = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(1, 1, N, device="cuda")
+    err = cuda_err()
+    _lib.vsa_sparse_attn_fwd(_lib.qkvo(q, k, v, o, lse), None, kinds, idx, cnt, 3, shape, 0.0, err)
+    grads, e = _run_lists(shape, q, k, v, do, o, lse, kinds, idx, cnt, 3)
+    assert e == 0 and _lib.vsa_get_device_error(err) == 0
+    lists = [x[x >= 0].tolist() for x in idx.cpu()]
+    for b in (0, 1, 2849, 2850, 5631, 5632, 5698, 5699):
+        # every query block that keeps b or is b, every key block that these keep
+        rows = sorted({b} | {j for j, x in enumerate(lists) if b in x})
+        keys = sorted({x for j in rows for x in lists[j]})
+        at = lambda bs: torch.cat([torch.arange(x * block, min(N, (x + 1) * block)) for x in bs]).cuda()  # noqa: E731
+        qi, ki = at(rows), at(keys)
+        al = torch.tensor([[x in lists[j] for x in keys] for j in rows])
+        al = al.cuda()[torch.searchsorted(torch.tensor(rows).cuda(), qi // block)][:, torch.searchsorted(torch.tensor(keys).cuda(), ki // block)]
+        _, _, want, bounds = reference(q[0, 0, qi], k[0, 0, ki], v[0, 0, ki], do[0, 0, qi], al, o=o[0, 0, qi], lse=lse[0, 0, qi])
+        mine, key = qi // block == b, ki // block == b
+        pick = (mine, key, key)
+        assert_grads([grads[0][0, 0, qi][mine], grads[1][0, 0, ki][key], grads[2][0, 0, ki][key]],
+                     [w[m] for w, m in zip(want, pick)], [w[m] for w, m in zip(bounds, pick)], f"block {b}")
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements a tensor: the last head is computed as the same head alone."""
+    H, N, d = 142, 118800, 128
+    assert H * N * d > 1 << 31
+    nb = -(-N // 128)
+    shape, one = (_lib.make_shape(1, h, 1, 1, N, d, 128) for h in (H, 1))
+    idx = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, 1, nb, 1).repeat(1, H, 1, 1)
+    cnt = torch.ones(1, H, nb, dtype=torch.int32, device="cuda")
+    kinds = torch.zeros(H, dtype=torch.uint8, device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    full = [torch.zeros(1, H, N, d, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+    last = [torch.randn(1, 1, N, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    lse = torch.zeros(1, H, N, device="cuda")
+    o, l1 = torch.empty_like(last[0]), torch.empty(1, 1, N, device="cuda")
+    err = cuda_err()
+    _lib.vsa_sparse_attn_fwd(_lib.qkvo(*last[:3], o, l1), None, kinds[:1], idx[:, :1], cnt[:, :1], 1, one, 0.0, err)
+    for t, x in zip(full, (*last, o)):
+        t[:, -1:] = x
+    lse[:, -1:] = l1
+    q, k, v, do, ofull = full
+    grads, e = _run_lists(shape, q, k, v, do, ofull, lse, kinds, idx, cnt, 1)
+    want, e1 = _run_lists(one, *last, o, l1, kinds[:1], idx[:, :1].contiguous(), cnt[:, :1].contiguous(), 1)
+    assert e == 0 and e1 == 0 and _lib.vsa_get_device_error(err) == 0
+    for a, b in zip(grads, want):
+        assert torch.equal(a[:, -1:], b) and bool((a[:, :3] == 0).all())
+
+
+def test_semantic_layouts():
+    """Query and key rows in orders of their own (the semantic permutation's steps): gather, lists, gradient, scatter."""
+    H, N, d, C = 2, 700, 128, 12
+    wl = synthetic.Workload("sem", 1, H, 5, 10, 14, d, 128, "bf16", "semantic")
+    q, k, v = (x.cuda() for x in synthetic.make_qkv(wl))
+    do = _rows(q.shape, 31)
+    shape = _lib.make_shape(1, H, 5, 10, 14, d, 128)
+    nblk, err = _lib.vsa_num_blocks(shape), cuda_err()
+    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.empty(max(_lib.vsa_kmeans_workspace_size(shape, C), _lib.vsa_semantic_mask_workspace_size(shape)), dtype=torch.uint8,
+                     device="cuda")
+    found = []
+    for x in (q, k):
+        f = (torch.empty(H, C, d, device="cuda"), i32(H, N), i32(H, C), i32(H, N))
+        _lib.vsa_kmeans(x, shape, C, 3, *f, ws, ws.numel(), err)
+        found.append(f)
+    keep, bits, idx, cnt = i32(H, C, 1), i32(1, H, nblk, 1), i32(1, H, nblk, nblk), i32(1, H, nblk)
+    (cq, lq, nq, pq), (ck, lk, nk, pk) = found
+    _lib.vsa_semantic_mask(cq, nq, lq, pq, C, ck, nk, lk, pk, C, shape, 0.5, 0.0, keep, bits, idx, cnt, nblk, ws, ws.numel(), err)
+    p = [torch.empty_like(q) for _ in range(8)]
+    for src, perm, dst in ((q, pq, p[0]), (k, pk, p[1]), (v, pk, p[2]), (do, pq, p[3])):
+        _lib.vsa_gather_rows(src, perm, dst, shape, err)
+    lse = torch.empty(1, H, N, device="cuda")
+    kinds = torch.ones(H, dtype=torch.uint8, device="cuda")
+    _lib.vsa_sparse_attn_fwd(_lib.qkvo(*p[:3], p[4], lse), _lib.qkvo(*p[:3], p[4], lse), kinds, idx, cnt, nblk, shape, 0.0, err)
+    bws = torch.empty(_lib.vsa_sparse_attn_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    s = _lib.qkvo_grad(p[0], p[1], p[2], p[4], p[3], lse, p[5], p[6], p[7])
+    _lib.vsa_sparse_attn_bwd(s, s, kinds, idx, cnt, nblk, shape, 0.0, bws, bws.numel(), err)
+    grads = [torch.empty_like(q) for _ in range(3)]
+    for src, perm, dst in ((p[5], pq, grads[0]), (p[6], pk, grads[1]), (p[7], pk, grads[2])):
+        _lib.vsa_scatter_rows(src, None, perm, dst, None, shape, err)
+    assert _lib.vsa_get_device_error(err) == 0
+    for h in range(H):
+        slot_q, slot_k = pq[h].long().argsort(), pk[h].long().argsort()
+        mask = torch.zeros(nblk, nblk, dtype=torch.bool, device="cuda")
+        for i in range(nblk):
+            mask[i, idx[0, h, i, :int(cnt[0, h, i])].long()] = True
+        assert 0 < int(mask.sum()) < nblk * nblk
+        al = allowed_blocks(mask, slot_q, 128, slot_k)
+        _, _, want, bounds = reference(q[0, h], k[0, h], v[0, h], do[0, h], al, o=p[4][0, h][slot_q], lse=lse[0, h][slot_q])
+        assert_grads([x[0, h] for x in grads], want, bounds, f"head {h}")
+
+
 def test_refusals():
     q = torch.zeros(1, 2, 256, 64, dtype=torch.bfloat16, device="cuda")
     lse = torch.zeros(1, 2, 256, device="cuda")

@@ -195,6 +195,28 @@ def test_backward_heads_and_strides(dtype):
                    _rand(1, 1, 200000, 64, seed=8, dtype=dtype), None)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows come out as they do alone, and the first are not touched by them."""
+    B, H, N, d = 1, 137, 122500, 128
+    assert B * H * N * d > 1 << 31
+    x = torch.zeros(B, N, H, d, dtype=BF, device="cuda")
+    x[:, -300:] = _rand(B, 300, H, d, seed=1)
+    w, dy = _rand(d, seed=2), torch.zeros(B, H, N, d, dtype=BF, device="cuda")
+    dy[:, :, -300:] = _rand(B, H, 300, d, seed=3)
+    tail = x[:, -300:].contiguous().transpose(1, 2)
+    full, part = (vsa.RMSNorm(B, H, n, d, with_grad=True) for n in (N, 300))
+    r, p = full(x.transpose(1, 2), w), part(tail, w)
+    assert torch.equal(r.y[:, :, -300:], p.y) and torch.equal(r.rstd[:, :, -300:], p.rstd) and bool((r.y[:, :, :1000] == 0).all())
+    rstd = r.rstd
+    del r
+    dx, dw = full.backward(dy, x.transpose(1, 2), rstd, w)
+    px, pw = part.backward(dy[:, :, -300:].contiguous(), tail, p.rstd, w)
+    assert torch.equal(dx[:, :, -300:], px) and bool((dx[:, :, :1000] == 0).all())
+    # two fp32 sums of the same terms, each within 2^-15 of the sum of their sizes
+    terms = (dy[:, :, -300:].double() * tail.double() * p.rstd.double()[..., None]).abs().sum((0, 1, 2))
+    _near(dw, pw.double(), terms * 2.0 ** -14, "dw")
+
+
 def test_normalise_is_differentiable():
     """autograd through x, weight and residual, one output or both, against torch's gradients in 64 bits."""
     B, H, N, d = 1, 2, 40, 128
