@@ -22,6 +22,7 @@ from ._lib import (VSA_BF16, VSA_CUBE, VSA_F32, VSA_SELECT_CUBE, VSA_SELECT_GIVE
                    vsa_sparse_attn_fwd, vsa_sparse_attn_fwd_natural, vsa_unpermute, SemParams, make_sem_params,
                    vsa_quantize_fp8, vsa_sparse_attn_fwd_fp8qk, QKVOGrad, qkvo_grad, vsa_sparse_attn_bwd,
                    vsa_sparse_attn_bwd_workspace_size, vsa_attention_bwd, vsa_attention_bwd_workspace_size,
+                   vsa_attention_train, vsa_attention_train_workspace_size,
                    NormShape, make_norm_shape, vsa_rms_norm, vsa_rms_norm_bwd, vsa_rms_norm_bwd_workspace_size,
                    vsa_gather_rows, vsa_kmeans, vsa_kmeans_workspace_size, vsa_scatter_rows, vsa_semantic_attention,
                    vsa_semantic_mask, vsa_semantic_mask_workspace_size, vsa_semantic_workspace_size)
@@ -127,9 +128,10 @@ class _Attend(torch.autograd.Function):
     def forward(ctx, plan, q, k, v, kinds):
         ctx.set_materialize_grads(False)
         with _on(None, plan.device):
-            o, lse = plan(q, k, v, kinds=kinds)
+            o_lo = torch.empty_like(q, memory_format=torch.contiguous_format)
+            o, lse = plan(q, k, v, kinds=kinds, o_lo=o_lo)
             ctx.plan = plan
-            ctx.save_for_backward(q, k, v, o, lse, plan.kinds.clone())
+            ctx.save_for_backward(q, k, v, o, lse, plan.kinds.clone(), o_lo)
         return o
 
     @staticmethod
@@ -138,8 +140,8 @@ class _Attend(torch.autograd.Function):
         if d_o is None:
             return (None,) * 5
         _no_capture("attend")
-        q, k, v, o, lse, kinds = ctx.saved_tensors
-        grads = ctx.plan.backward(d_o.contiguous(), q, k, v, o, lse, kinds=kinds)
+        q, k, v, o, lse, kinds, o_lo = ctx.saved_tensors
+        grads = ctx.plan.backward(d_o.contiguous(), q, k, v, o, lse, kinds=kinds, o_lo=o_lo)
         return (None, *(g if need else None for g, need in zip(grads, ctx.needs_input_grad[1:4])), None)
 
 
@@ -155,7 +157,9 @@ class SparseAttention(_HostPipelined):
     qk_fp8:  Q.K^T on e4m3 codes with one power-of-two scale per block; P.V stays bf16
              (bf16, d = 128, block 128).
     with_grad: the plan also holds the workspace of the gradient (``backward``, ``attend``); the
-             call then always returns its log-sum-exp.  Not with qk_fp8.
+             call then always returns its log-sum-exp, and fills ``o_lo``, where it is given, with
+             what rounding the output to bf16 left over (for a more exact gradient).  Not with
+             qk_fp8.
 
     A plan's workspaces serve one call at a time: order calls on different streams, and graphs
     that captured them, before they run, or give each its own plan.
@@ -185,7 +189,8 @@ class SparseAttention(_HostPipelined):
             w_t = w_t_t if w_t is None else w_t
         self.w_s, self.w_t = int(w_s or 0), int(w_t or 0)
         self.params = make_params(self.w_s, self.w_t, profile_frac, topk, scale, layout_in_kernel, qk_fp8)
-        self.ws_bytes = vsa_attention_workspace_size(self.shape, self.params, _DTYPE[dtype], self.select)
+        size = vsa_attention_train_workspace_size if with_grad else vsa_attention_workspace_size
+        self.ws_bytes = size(self.shape, self.params, _DTYPE[dtype], self.select)
         if self.ws_bytes == 0:
             raise VsaError(_lib.VSA_ERR_INVALID_ARG, "vsa_attention_workspace_size")
         off_bits, off_idx, off_cnt, self.max_kv = vsa_attention_workspace_layout(self.shape, self.params,
@@ -211,8 +216,11 @@ class SparseAttention(_HostPipelined):
             self.kinds_bwd = torch.full((B * H,), VSA_CUBE, dtype=torch.uint8, device=self.device)
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: Optional[torch.Tensor] = None,
-                 lse: Optional[torch.Tensor] = None, kinds: Optional[torch.Tensor] = None, stream=None):
-        for t in (q, k, v):
+                 lse: Optional[torch.Tensor] = None, kinds: Optional[torch.Tensor] = None, stream=None,
+                 o_lo: Optional[torch.Tensor] = None):
+        if o_lo is not None and not self.with_grad:
+            raise ValueError("o_lo needs with_grad=True")
+        for t in (q, k, v) if o_lo is None else (q, k, v, o_lo):
             if t.dtype != self.dtype or t.device != self.device or not t.is_contiguous():
                 raise ValueError("q, k, v must be contiguous tensors of the configured dtype and device")
             if tuple(t.shape) != (self.B, self.H, self.N, self.d):
@@ -225,15 +233,19 @@ class SparseAttention(_HostPipelined):
             if kinds is None:
                 raise ValueError("select='given' needs kinds")
             self.kinds.copy_(kinds.reshape(-1).to(torch.uint8))
-        vsa_attention(qkvo(q, k, v, out, lse), _DTYPE[self.dtype], self.shape, self.params, self.select, self.kinds,
-                      self.mse, self.ws, self.ws_bytes, self.err, stream)
+        if o_lo is not None:
+            vsa_attention_train(qkvo(q, k, v, out, lse), o_lo, _DTYPE[self.dtype], self.shape, self.params, self.select,
+                                self.kinds, self.mse, self.ws, self.ws_bytes, self.err, stream)
+        else:
+            vsa_attention(qkvo(q, k, v, out, lse), _DTYPE[self.dtype], self.shape, self.params, self.select, self.kinds,
+                          self.mse, self.ws, self.ws_bytes, self.err, stream)
         return (out, lse) if self.with_lse else out
 
     def backward(self, d_o: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                  lse: torch.Tensor, kinds: Optional[torch.Tensor] = None, d_lse: Optional[torch.Tensor] = None,
-                 out: Optional[Sequence[torch.Tensor]] = None, stream=None):
-        """Gradients (dq, dk, dv) of a call of this plan, from its inputs, its outputs and the gradients
-        of those.  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
+                 out: Optional[Sequence[torch.Tensor]] = None, stream=None, o_lo: Optional[torch.Tensor] = None):
+        """Gradients (dq, dk, dv) of a call of this plan, from its inputs, its outputs (``o_lo`` among
+        them, where the call filled it) and the gradients of those.  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
         where another call comes between); they are not needed for select="cube".  Nothing else of the
         call is kept: the masks are built again.  Asynchronous on ``stream``; can be captured."""
         if not self.with_grad:
@@ -244,7 +256,7 @@ class SparseAttention(_HostPipelined):
                 out = tuple(torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(3))
             if len(out) != 3:
                 raise ValueError("out is (dq, dk, dv)")
-            for t in (d_o, q, k, v, o, *out):
+            for t in (d_o, q, k, v, o, *out) if o_lo is None else (d_o, q, k, v, o, *out, o_lo):
                 if t.dtype != self.dtype or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != shape:
                     raise ValueError(f"contiguous {self.dtype} tensors of shape {shape} on {self.device} expected")
             for t in (lse, d_lse):
@@ -257,14 +269,14 @@ class SparseAttention(_HostPipelined):
                 if kinds.numel() != self.B * self.H:
                     raise ValueError(f"{self.B * self.H} kinds expected")
                 self.kinds_bwd.copy_(kinds.reshape(-1).to(torch.uint8))
-            vsa_attention_bwd(qkvo_grad(q, k, v, o, d_o, lse, *out, d_lse=d_lse), _DTYPE[self.dtype], self.shape,
+            vsa_attention_bwd(qkvo_grad(q, k, v, o, d_o, lse, *out, d_lse=d_lse, o_lo=o_lo), _DTYPE[self.dtype], self.shape,
                               self.params, self.kinds_bwd, self.ws_bwd, self.ws_bwd_bytes, self.err)
         return tuple(out)
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kinds: Optional[torch.Tensor] = None):
         """The call as a differentiable function: o whose ``backward`` fills the gradients of q, k and v
-        (first derivatives; the masks count as constants).  Keeps q, k, v, o, the log-sum-exp and the
-        kinds for the gradient.  Where autograd records it is refused under graph capture: capture
+        (first derivatives; the masks count as constants).  Keeps q, k, v, o, o_lo, the log-sum-exp and
+        the kinds for the gradient.  Where autograd records it is refused under graph capture: capture
         the call itself and ``backward`` instead."""
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
@@ -530,6 +542,7 @@ __all__ = ["SparseAttention", "SemanticAttention", "attention", "SemParams", "ma
            "vsa_profile_workspace_size", "vsa_sparse_attn_fwd", "vsa_sparse_attn_fwd_natural", "vsa_unpermute",
            "vsa_quantize_fp8", "vsa_sparse_attn_fwd_fp8qk", "QKVOGrad", "qkvo_grad", "vsa_sparse_attn_bwd",
            "vsa_sparse_attn_bwd_workspace_size", "vsa_attention_bwd", "vsa_attention_bwd_workspace_size",
+           "vsa_attention_train", "vsa_attention_train_workspace_size",
            "RMSNorm", "NormOut", "NormShape", "make_norm_shape", "vsa_rms_norm", "vsa_rms_norm_bwd",
            "vsa_rms_norm_bwd_workspace_size", "VSA_SPATIAL", "VSA_TEMPORAL",
            "VSA_CUBE", "VSA_F32", "VSA_BF16", "VSA_SELECT_PROFILE", "VSA_SELECT_GIVEN", "VSA_SELECT_CUBE"]

@@ -57,7 +57,7 @@ class QKVO(ctypes.Structure):
 
 
 class QKVOGrad(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "d_o", "lse", "d_lse", "dq", "dk", "dv")]
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "d_o", "lse", "d_lse", "dq", "dk", "dv", "o_lo")]
 
 
 class NormShape(ctypes.Structure):
@@ -102,6 +102,8 @@ def _load():
         "vsa_sparse_attn_bwd_workspace_size": (sz, [P(Shape)]),
         "vsa_sparse_attn_bwd": (st, [P(QKVOGrad), P(QKVOGrad), vp, vp, vp, i32, P(Shape), ctypes.c_float, vp, sz, vp,
                                      vp]),
+        "vsa_attention_train_workspace_size": (sz, [P(Shape), P(Params), i32, i32]),
+        "vsa_attention_train": (st, [P(QKVO), vp, i32, P(Shape), P(Params), i32, vp, vp, vp, sz, vp, vp]),
         "vsa_attention_bwd_workspace_size": (sz, [P(Shape), P(Params), i32]),
         "vsa_attention_bwd": (st, [P(QKVOGrad), i32, P(Shape), P(Params), vp, vp, sz, vp, vp]),
         "vsa_rms_norm": (st, [vp, vp, i32, vp, i32, P(NormShape), vp, vp, vp, vp, vp, vp]),
@@ -323,9 +325,20 @@ def vsa_attention(io: QKVO, dtype: int, shape: Shape, params: Params, select: in
 # gradients
 # ---------------------------------------------------------------------------------------
 
-def qkvo_grad(q, k, v, o, d_o, lse, dq, dk, dv, d_lse=None) -> QKVOGrad:
+def qkvo_grad(q, k, v, o, d_o, lse, dq, dk, dv, d_lse=None, o_lo=None) -> QKVOGrad:
     return QKVOGrad(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(d_lse), _ptr(dq), _ptr(dk),
-                    _ptr(dv))
+                    _ptr(dv), _ptr(o_lo))
+
+
+def vsa_attention_train_workspace_size(shape: Shape, params: Params, dtype: int, select: int) -> int:
+    return int(lib.vsa_attention_train_workspace_size(ctypes.byref(shape), ctypes.byref(params), dtype, select))
+
+
+def vsa_attention_train(io: QKVO, o_lo, dtype: int, shape: Shape, params: Params, select: int, kinds, mse, ws, ws_bytes,
+                        err, stream=None):
+    _check(lib.vsa_attention_train(ctypes.byref(io), _ptr(o_lo), dtype, ctypes.byref(shape), ctypes.byref(params), select,
+                                   _ptr(kinds), _ptr(mse), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)),
+           "vsa_attention_train")
 
 
 def vsa_sparse_attn_bwd_workspace_size(shape: Shape) -> int:

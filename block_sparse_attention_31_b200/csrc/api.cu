@@ -412,7 +412,8 @@ struct Fp8QK {
 static vsa_status sparse_attn_fwd_impl(const vsa_qkvo* natural, const vsa_qkvo* permuted, const Fp8QK& f8,
                                        const uint8_t* d_kind, const int32_t* d_kv_idx, const int32_t* d_kv_cnt,
                                        int max_kv, const int32_t* d_order, const vsa_shape* shape, float scale,
-                                       int* d_err, cudaStream_t stream) {
+                                       int* d_err, cudaStream_t stream, void* lo_nat = nullptr,
+                                       void* lo_perm = nullptr) {
   Geom g;
   vsa_status st = make_geom(shape, &g);
   if (st != VSA_OK) return st;
@@ -468,6 +469,8 @@ static vsa_status sparse_attn_fwd_impl(const vsa_qkvo* natural, const vsa_qkvo* 
   a.kexp = qk8 ? f8.kexp : nullptr;
   a.nat_q = a.nat_k = a.nat_v = nullptr;
   a.nat_o = natural->o;  // written only for a head with an invalid kind byte (zero rows)
+  a.lo_nat = lo_nat;
+  a.lo_perm = permuted != nullptr ? lo_perm : lo_nat;
   const cudaError_t e = launch_sparse_attn(nat, perm, a, shape->d, stream);
   return e == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
@@ -505,9 +508,10 @@ vsa_status vsa_quantize_fp8(const void* natural, const void* permuted, const uin
   return e == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
-vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo* natural, const uint8_t* d_kind, const int32_t* d_kv_idx,
-                                       const int32_t* d_kv_cnt, int max_kv, const int32_t* d_order,
-                                       const vsa_shape* shape, float scale, int* d_err, cudaStream_t stream) {
+static vsa_status sparse_attn_fwd_natural_impl(const vsa_qkvo* natural, const uint8_t* d_kind,
+                                               const int32_t* d_kv_idx, const int32_t* d_kv_cnt, int max_kv,
+                                               const int32_t* d_order, const vsa_shape* shape, float scale, int* d_err,
+                                               cudaStream_t stream, void* lo) {
   Geom g;
   vsa_status st = make_geom(shape, &g);
   if (st != VSA_OK) return st;
@@ -541,8 +545,16 @@ vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo* natural, const uint8_t* d
   a.nat_k = natural->k;
   a.nat_v = natural->v;
   a.nat_o = natural->o;
+  a.lo_nat = a.lo_perm = lo;
   const cudaError_t e = launch_sparse_attn(nat, nat, a, shape->d, stream);
   return e == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo* natural, const uint8_t* d_kind, const int32_t* d_kv_idx,
+                                       const int32_t* d_kv_cnt, int max_kv, const int32_t* d_order,
+                                       const vsa_shape* shape, float scale, int* d_err, cudaStream_t stream) {
+  return sparse_attn_fwd_natural_impl(natural, d_kind, d_kv_idx, d_kv_cnt, max_kv, d_order, shape, scale, d_err, stream,
+                                      nullptr);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -572,7 +584,8 @@ static vsa_status check_grad(const vsa_qkvo_grad* t) {
 }
 
 static bool grad_on_device(const vsa_qkvo_grad* t) {
-  return on_current_device({t->q, t->k, t->v, t->o, t->d_o, t->lse, t->d_lse, t->dq, t->dk, t->dv});
+  return aligned16(t->o_lo) &&
+         on_current_device({t->q, t->k, t->v, t->o, t->d_o, t->lse, t->d_lse, t->dq, t->dk, t->dv, t->o_lo});
 }
 
 static vsa_status encode_bwd_set(BwdMaps* m, const vsa_qkvo_grad* t, const Geom& g, int rows, int BH, int d) {
@@ -605,11 +618,13 @@ static vsa_status sparse_attn_bwd_impl(const vsa_qkvo_grad* natural, const vsa_q
   p.kv_cnt = d_kv_cnt;
   p.o_nat = rows->o;
   p.do_nat = rows->d_o;
+  p.lo_nat = rows->o_lo;
   p.lse_nat = rows->lse;
   p.dlse_nat = rows->d_lse;
   if (permuted != nullptr) {
     p.o_perm = permuted->o;
     p.do_perm = permuted->d_o;
+    p.lo_perm = permuted->o_lo;
     p.lse_perm = permuted->lse;
     p.dlse_perm = permuted->d_lse;
   }
@@ -1062,12 +1077,16 @@ vsa_status vsa_attention_workspace_layout(const vsa_shape* shape, const vsa_para
   return VSA_OK;
 }
 
-vsa_status vsa_attention(const vsa_qkvo* io, vsa_dtype dtype, const vsa_shape* shape, const vsa_params* params,
-                         vsa_select select, uint8_t* d_kind, float* d_mse, void* ws, size_t ws_bytes, int* d_err,
-                         cudaStream_t stream) {
+// o_lo: O's rounding errors in natural order (dtype rows), or null; their permuted rows follow vsa_attention's own
+// workspace.
+static vsa_status attention_impl(const vsa_qkvo* io, void* o_lo, vsa_dtype dtype, const vsa_shape* shape,
+                                 const vsa_params* params, vsa_select select, uint8_t* d_kind, float* d_mse, void* ws,
+                                 size_t ws_bytes, int* d_err, cudaStream_t stream) {
   AttnLayout L;
   vsa_status st = attention_layout(shape, params, dtype, select, &L);
   if (st != VSA_OK) return st;
+  void* plo = static_cast<uint8_t*>(ws) + L.bytes;
+  if (o_lo != nullptr) L.bytes = vsa_attention_train_workspace_size(shape, params, dtype, select);
   if ((st = check_qkvo(io)) != VSA_OK) return st;
   if (!d_kind || !ws || !d_err || !aligned16(ws)) return VSA_ERR_INVALID_ARG;
   if (ws_bytes < L.bytes) return VSA_ERR_WORKSPACE;
@@ -1099,8 +1118,8 @@ vsa_status vsa_attention(const vsa_qkvo* io, vsa_dtype dtype, const vsa_shape* s
     if ((st = vsa_build_mask(d_kind, nullptr, nullptr, shape, params, bits, kv_idx, kv_cnt, L.max_kv, nullptr, 0,
                              d_err, stream)) != VSA_OK)
       return st;
-    return vsa_sparse_attn_fwd_natural(io, d_kind, kv_idx, kv_cnt, L.max_kv, nullptr, shape, params->scale, d_err,
-                                       stream);
+    return sparse_attn_fwd_natural_impl(io, d_kind, kv_idx, kv_cnt, L.max_kv, nullptr, shape, params->scale, d_err,
+                                        stream, o_lo);
   }
   // 2. layouts
   const vsa_dtype src_t = dtype;
@@ -1127,15 +1146,45 @@ vsa_status vsa_attention(const vsa_qkvo* io, vsa_dtype dtype, const vsa_shape* s
     st = vsa_sparse_attn_fwd_fp8qk(io, &perm_set, q8, qe, k8, ke, d_kind, kv_idx, kv_cnt, L.max_kv, order, shape,
                                    params->scale, d_err, stream);
   } else if (dtype == VSA_F32) {
-    st = vsa_sparse_attn_fwd(&perm_set, nullptr, d_kind, kv_idx, kv_cnt, L.max_kv, order, shape, params->scale,
-                             d_err, stream);
+    st = sparse_attn_fwd_impl(&perm_set, nullptr, Fp8QK{nullptr, nullptr, nullptr, nullptr}, d_kind, kv_idx, kv_cnt,
+                              L.max_kv, order, shape, params->scale, d_err, stream, o_lo != nullptr ? plo : nullptr);
   } else {
-    st = vsa_sparse_attn_fwd(io, &perm_set, d_kind, kv_idx, kv_cnt, L.max_kv, order, shape, params->scale, d_err,
-                             stream);
+    st = sparse_attn_fwd_impl(io, &perm_set, Fp8QK{nullptr, nullptr, nullptr, nullptr}, d_kind, kv_idx, kv_cnt,
+                              L.max_kv, order, shape, params->scale, d_err, stream, o_lo,
+                              o_lo != nullptr ? plo : nullptr);
   }
   if (st != VSA_OK) return st;
   // 5. back to natural order
-  return vsa_unpermute(po, plse, io->o, dtype, io->lse, d_kind, shape, d_err, stream);
+  if ((st = vsa_unpermute(po, plse, io->o, dtype, io->lse, d_kind, shape, d_err, stream)) != VSA_OK || o_lo == nullptr)
+    return st;
+  return vsa_unpermute(plo, nullptr, o_lo, dtype, nullptr, d_kind, shape, d_err, stream);
+}
+
+vsa_status vsa_attention(const vsa_qkvo* io, vsa_dtype dtype, const vsa_shape* shape, const vsa_params* params,
+                         vsa_select select, uint8_t* d_kind, float* d_mse, void* ws, size_t ws_bytes, int* d_err,
+                         cudaStream_t stream) {
+  return attention_impl(io, nullptr, dtype, shape, params, select, d_kind, d_mse, ws, ws_bytes, d_err, stream);
+}
+
+size_t vsa_attention_train_workspace_size(const vsa_shape* shape, const vsa_params* params, vsa_dtype dtype,
+                                          vsa_select select) {
+  AttnLayout L;
+  Geom g;
+  if (attention_layout(shape, params, dtype, select, &L) != VSA_OK || make_geom(shape, &g) != VSA_OK) return 0;
+  if (params->qk_fp8 != 0) return 0;
+  return align256(L.bytes + static_cast<size_t>(shape->B) * shape->H * g.R * shape->d * 2);
+}
+
+vsa_status vsa_attention_train(const vsa_qkvo* io, void* o_lo, vsa_dtype dtype, const vsa_shape* shape,
+                               const vsa_params* params, vsa_select select, uint8_t* d_kind, float* d_mse, void* ws,
+                               size_t ws_bytes, int* d_err, cudaStream_t stream) {
+  if (o_lo == nullptr || !aligned16(o_lo) || io == nullptr || io->lse == nullptr || o_lo == io->o)
+    return VSA_ERR_INVALID_ARG;
+  if (params != nullptr && params->qk_fp8 != 0) return VSA_ERR_UNSUPPORTED;
+  vsa_status st = check_qkvo(io);
+  if (st != VSA_OK) return st;
+  if (!on_current_device({o_lo})) return VSA_ERR_INVALID_ARG;
+  return attention_impl(io, o_lo, dtype, shape, params, select, d_kind, d_mse, ws, ws_bytes, d_err, stream);
 }
 
 // Workspace of vsa_attention_bwd: the masks, the permuted q, k, v, dO, dq, dk, dv, the mask and the

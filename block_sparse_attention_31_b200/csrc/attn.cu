@@ -101,6 +101,11 @@ constexpr uint32_t kInTile0 = 1u << 30, kInTile1 = 1u << 31, kPartial = 1u << 29
 #endif
 constexpr int kPolyPairs8 = VSA_POLY_PAIRS8;
 
+// What is left of a pair after its rounding to bf16.
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t rounded) {
+  return pack_bf16x2(lo - __uint_as_float(rounded << 16), hi - __uint_as_float(rounded & 0xffff0000u));
+}
+
 // One CTA per pair of consecutive query blocks (tiles 0 and 1) of one head.  The K/V blocks
 // of the union of the two lists stream through a 2-stage ring once and serve both tiles; the
 // MMA issuer interleaves the tiles (P.V of one, then Q.K^T of the same tile, then the other
@@ -641,6 +646,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int tok = gather ? (slot % g.F) * g.S + slot / g.F : slot;
       __nv_bfloat16* orow = gather ? static_cast<__nv_bfloat16*>(a.nat_o) + (static_cast<size_t>(bh) * g.N + tok) * D
                                    : nullptr;
+      __nv_bfloat16* lrow = static_cast<__nv_bfloat16*>(use_perm ? a.lo_perm : a.lo_nat);
+      if (lrow != nullptr) lrow += (static_cast<size_t>(bh) * lse_stride + tok) * D;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -659,6 +666,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             v4.z = pack_bf16x2(o[q4 * 8 + 4] * inv, o[q4 * 8 + 5] * inv);
             v4.w = pack_bf16x2(o[q4 * 8 + 6] * inv, o[q4 * 8 + 7] * inv);
             const int col = c * 32 + q4 * 8;
+            if (lrow != nullptr && row_live)
+              *reinterpret_cast<uint4*>(lrow + col) =
+                  make_uint4(pack_rest(o[q4 * 8 + 0] * inv, o[q4 * 8 + 1] * inv, v4.x),
+                             pack_rest(o[q4 * 8 + 2] * inv, o[q4 * 8 + 3] * inv, v4.y),
+                             pack_rest(o[q4 * 8 + 4] * inv, o[q4 * 8 + 5] * inv, v4.z),
+                             pack_rest(o[q4 * 8 + 6] * inv, o[q4 * 8 + 7] * inv, v4.w));
             if (gather) {
               if (row_live) *reinterpret_cast<uint4*>(orow + col) = v4;
             } else {

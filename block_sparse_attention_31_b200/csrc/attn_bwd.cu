@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
   const long long first = static_cast<long long>(blockIdx.x - a.mask_ctas) * (groups * kPrepRows) + threadIdx.x / tpr;
   const long long all = static_cast<long long>(a.BH) * slots;
   const int c = threadIdx.x % tpr;
-  uint4 o[kPrepRows][2], go[kPrepRows][2];
+  uint4 o[kPrepRows][2], go[kPrepRows][2], lo[kPrepRows][2];
   float lse[kPrepRows], dlse[kPrepRows];
   bool has[kPrepRows];
 #pragma unroll
@@ -673,11 +673,14 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
     const size_t row = static_cast<size_t>(bh) * stride + (has[r] ? (a.by_token ? token : slot) : 0);
     const void* po = perm ? a.o_perm : a.o_nat;
     const void* pg = perm ? a.do_perm : a.do_nat;
+    const void* pl = perm ? a.lo_perm : a.lo_nat;
     const float* dl = perm ? a.dlse_perm : a.dlse_nat;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       o[r][j] = load8(po, row * a.d + (j * tpr + c) * 8, a.f32);
       go[r][j] = load8(pg, row * a.d + (j * tpr + c) * 8, a.f32);
+      lo[r][j] = make_uint4(0, 0, 0, 0);
+      if (pl != nullptr) lo[r][j] = load8(pl, row * a.d + (j * tpr + c) * 8, a.f32);
     }
     lse[r] = (perm ? a.lse_perm : a.lse_nat)[row];
     dlse[r] = 0.f;
@@ -685,7 +688,8 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
   }
 #pragma unroll
   for (int r = 0; r < kPrepRows; ++r) {
-    float delta = dot8(o[r][0], go[r][0]) + dot8(o[r][1], go[r][1]);
+    float delta = (dot8(o[r][0], go[r][0]) + dot8(o[r][1], go[r][1])) +
+                  (dot8(lo[r][0], go[r][0]) + dot8(lo[r][1], go[r][1]));
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1)
       if (off < tpr) delta += __shfl_xor_sync(0xffffffffu, delta, off);

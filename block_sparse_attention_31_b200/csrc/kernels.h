@@ -79,6 +79,9 @@ struct AttnArgs {
   const void* nat_k;
   const void* nat_v;
   void* nat_o;
+  // What rounding O to bf16 left over, as bf16 rows beside O's (null: not wanted)
+  void* lo_nat;
+  void* lo_perm;
 };
 
 cudaError_t launch_sparse_attn(const AttnMaps& nat, const AttnMaps& perm, const AttnArgs& a, int d,
@@ -95,6 +98,7 @@ struct BwdPrep {
   const int32_t* kv_idx;
   const int32_t* kv_cnt;
   const void *o_nat, *o_perm, *do_nat, *do_perm;
+  const void *lo_nat, *lo_perm;  // O's rounding errors, or null
   const float *lse_nat, *lse_perm, *dlse_nat, *dlse_perm;
   uint32_t* rbits;  // [BH, nblk, ceil(nblk / 32)] kept key blocks of every query block
   float* terms;     // [BH, nblk, 2, block]: -lse * log2 e (-inf: the row sees nothing), then -delta

@@ -390,6 +390,7 @@ typedef struct {
     const float *lse;             /* the forward call's log-sum-exp (required) */
     const float *d_lse;           /* gradient of lse, or NULL */
     void *dq, *dk, *dv;
+    const void *o_lo;             /* what rounding o to bf16 left over (vsa_attention_train), or NULL */
 } vsa_qkvo_grad;
 
 /* Workspace bytes of vsa_sparse_attn_bwd: a bitset of the lists (B*H*nblk*ceil(nblk/32) words)
@@ -398,10 +399,11 @@ VSA_API size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape *shape);
 
 /*
  * Gradient of vsa_sparse_attn_fwd: with P = exp(scale q k^T - lse) on the kept block pairs and
- * delta = rowsum(d_o * o) - d_lse,
+ * delta = rowsum(d_o * (o + o_lo)) - d_lse,
  *   dv = P^T d_o,   dS = P * (d_o v^T - delta),   dq = scale dS k,   dk = scale dS^T q.
  * P and dS are rounded to bf16 in front of their tensor products, every sum is fp32, the
- * gradients are bf16.  Each is written by one owner: two runs give the same bits.
+ * gradients are bf16.  Each is written by one owner: two runs give the same bits.  delta takes o as it is
+ * given: the error of a bf16 o moves a row's dq by that error times its mean key, which o_lo takes away.
  *   natural, permuted   as for vsa_sparse_attn_fwd (permuted may be NULL); bf16; padding slots
  *                       of cube layouts hold finite values, zero as vsa_permute leaves them.
  *                       Every row of a head's layout is written, rows that hold no token or
@@ -417,6 +419,21 @@ VSA_API vsa_status vsa_sparse_attn_bwd(const vsa_qkvo_grad *natural, const vsa_q
                                        int max_kv, const vsa_shape *shape, float scale, void *ws, size_t ws_bytes,
                                        int *d_err, cudaStream_t stream);
 
+/* Workspace bytes of vsa_attention_train (0 for invalid arguments or qk_fp8). */
+VSA_API size_t vsa_attention_train_workspace_size(const vsa_shape *shape, const vsa_params *params, vsa_dtype dtype,
+                                                  vsa_select select);
+
+/*
+ * vsa_attention for a call whose gradient is wanted: the same o and lse (required), and o_lo, what the rounding of
+ * o to bf16 left over, rounded to bf16 itself.
+ *   o_lo     [B, H, N, d] in dtype out, natural order
+ *   ws       vsa_attention_train_workspace_size bytes
+ *   the rest as vsa_attention; qk_fp8 returns VSA_ERR_UNSUPPORTED
+ */
+VSA_API vsa_status vsa_attention_train(const vsa_qkvo *io, void *o_lo, vsa_dtype dtype, const vsa_shape *shape,
+                                       const vsa_params *params, vsa_select select, uint8_t *d_kind, float *d_mse,
+                                       void *ws, size_t ws_bytes, int *d_err, cudaStream_t stream);
+
 /* Workspace bytes of vsa_attention_bwd (0 for invalid arguments or qk_fp8). */
 VSA_API size_t vsa_attention_bwd_workspace_size(const vsa_shape *shape, const vsa_params *params, vsa_dtype dtype);
 
@@ -424,7 +441,7 @@ VSA_API size_t vsa_attention_bwd_workspace_size(const vsa_shape *shape, const vs
  * Gradient of vsa_attention: permute -> masks -> vsa_sparse_attn_bwd -> unpermute, on `stream`.
  * The masks are built again from the kinds (and, for cube heads, from q and k), so nothing of
  * the forward call's workspace is needed.
- *   io       natural q, k, v, o, d_o, lse (d_lse or NULL); dq, dk, dv written; rows in dtype
+ *   io       natural q, k, v, o, d_o, lse (d_lse, o_lo or NULL); dq, dk, dv written; rows in dtype
  *   d_kind   [B*H] the kinds the forward call used (given, or as it wrote them)
  *   params   the forward call's; layout_in_kernel is accepted and changes nothing here, qk_fp8
  *            returns VSA_ERR_UNSUPPORTED (the e4m3 codes have no gradient)

@@ -16,10 +16,11 @@ ACC = 2.0 ** -15      # up to 128 fp32 additions at 2^-23 each, with room for th
 SUM = 2.0 ** -14      # fp32 sums over the keys or queries, relative to the sum of the absolute terms
 
 
-def reference(q, k, v, do, allowed, scale=None, d_lse=None, o=None, lse=None):
+def reference(q, k, v, do, allowed, scale=None, d_lse=None, o=None, lse=None, own_o=False):
     """One head in 64 bits on natural-order rows.  allowed: [N, N] bool, queries by keys.  o and lse:
-    the forward call's, where given; else the exact ones.  Returns o, lse, (dq, dk, dv) and their
-    bounds."""
+    the forward call's, where given; else the exact ones.  own_o: the kernel's delta comes from its own
+    O before its rounding, whose error is that of P (U + P_REL of every term).  Returns o, lse,
+    (dq, dk, dv) and their bounds."""
     q, k, v, do = (x.double() for x in (q, k, v, do))
     scale = 1 / math.sqrt(q.shape[1]) if scale is None else scale
     s = (q @ k.T * scale).masked_fill(~allowed, -math.inf)
@@ -37,6 +38,8 @@ def reference(q, k, v, do, allowed, scale=None, d_lse=None, o=None, lse=None):
     grads = (scale * ds @ k, scale * ds.T @ q, p.T @ do)
     e = ACC * ((do.abs() @ v.abs().T) + (do.abs() * o.abs()).sum(1)[:, None] +
                (d_lse.double().abs()[:, None] if d_lse is not None else 0.0))
+    if own_o:
+        e = e + (U + P_REL + SUM) * (do.abs() * (p @ v.abs())).sum(1)[:, None]
     w = (U + P_REL + SUM) * ds.abs() + 1.01 * p * e
     bounds = (scale * w @ k.abs() + U * grads[0].abs(), scale * w.T @ q.abs() + U * grads[1].abs(),
               (U + P_REL + SUM) * p.T @ do.abs() + U * grads[2].abs())

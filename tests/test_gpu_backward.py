@@ -160,10 +160,14 @@ def test_bad_lists_and_kinds():
 # ------------------------------------------------------------------------------------
 # the whole call
 # ------------------------------------------------------------------------------------
-def _plan_case(plan, wl, kinds_list, q, k, v, do, kinds=None, dtype=torch.bfloat16, d_lse=None):
-    """plan(q, k, v), then its gradients against 64 bits with the call's own O and LSE."""
-    o, lse = plan(q, k, v, kinds=kinds)
-    grads = plan.backward(do, q, k, v, o, lse, kinds=kinds if kinds is not None else plan.kinds, d_lse=d_lse)
+def _plan_case(plan, wl, kinds_list, q, k, v, do, kinds=None, d_lse=None, lo=False):
+    """plan(q, k, v), then its gradients against 64 bits: with the call's own O and LSE, or (lo) with what O's
+    rounding left over against the gradient of the exact attention too."""
+    o_lo = torch.full_like(q, 7.0) if lo else None
+    o, lse = plan(q, k, v, kinds=kinds, o_lo=o_lo)
+    plain = plan(q, k, v, kinds=kinds)
+    assert torch.equal(o, plain[0]) and torch.equal(lse, plain[1])
+    grads = plan.backward(do, q, k, v, o, lse, kinds=kinds if kinds is not None else plan.kinds, d_lse=d_lse, o_lo=o_lo)
     assert plan.device_error() == 0
     for b in range(wl.B):
         for h, kind in enumerate(kinds_list):
@@ -171,9 +175,16 @@ def _plan_case(plan, wl, kinds_list, q, k, v, do, kinds=None, dtype=torch.bfloat
             q16, k16, v16, do16, o16 = (x[b, h].to(torch.bfloat16) for x in (q, k, v, do, o))
             keep = keep_for_head(kind, wl, plan.w_s, plan.w_t, q16.cpu(), k16.cpu())
             al = allowed_blocks(keep, slots, wl.block).cuda()
-            _, _, want, bounds = reference(q16, k16, v16, do16, al, o=o16, lse=lse[b, h],
-                                           d_lse=None if d_lse is None else d_lse[b, h])
+            dl = None if d_lse is None else d_lse[b, h]
+            o64 = o16.double() + (o_lo[b, h].double() if lo else 0.0)
+            _, _, want, bounds = reference(q16, k16, v16, do16, al, o=o64, lse=lse[b, h], d_lse=dl)
             assert_grads([g[b, h] for g in grads], want, bounds, f"batch {b} head {h} kind {kind}")
+            if lo:
+                # the rest is smaller than half a step of what it was left over from
+                assert bool((o_lo[b, h].double().abs() <= o16.double().abs() * 2.0 ** -8 + 2.0 ** -133).all())
+                # lse is the kernel's: within 2^-12 + 2^-20 |lse| of the exact one, an error of P like that of its own
+                _, _, want, bounds = reference(q16, k16, v16, do16, al, d_lse=dl, own_o=True)
+                assert_grads([g[b, h] for g in grads], want, [1.1 * x for x in bounds], f"exact: batch {b} head {h} kind {kind}")
     return o, lse, grads
 
 
@@ -190,6 +201,7 @@ def test_call_pattern_heads(F, Hl, Wl, d, block, dtype):
         plan = vsa.SparseAttention(2, 2, F, Hl, Wl, d, block, dtype=dtype, select="given", w_s=1, w_t=9, with_grad=True,
                                    layout_in_kernel=layout)
         _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, d_lse=d_lse)
+        _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, lo=True)
 
 
 @pytest.mark.parametrize("F,Hl,Wl,topk", [(5, 5, 9, 3), (9, 9, 17, 4), (4, 4, 8, 2)])
@@ -199,6 +211,7 @@ def test_call_cube_heads(F, Hl, Wl, topk):
     do = _rows(q.shape, 11)
     plan = vsa.SparseAttention(1, 2, F, Hl, Wl, 128, 128, select="cube", topk=topk, cube=(4, 4, 8), with_grad=True)
     _plan_case(plan, wl, [C_, C_], q, k, v, do)
+    _plan_case(plan, wl, [C_, C_], q, k, v, do, lo=True)
 
 
 def test_call_profiled_heads():
@@ -220,14 +233,14 @@ def test_attend_matches_backward_and_differences():
     o = plan.attend(*leaves, kinds=kinds)
     other = plan.attend(*(x * 0.5 for x in (q, k, v)), kinds=1 - kinds)     # another call comes between
     o.backward(do)
-    o2, lse, grads = _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds)
+    o2, lse, grads = _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, lo=True)
     assert torch.equal(o.detach(), o2) and other.shape == o.shape
     for x, g in zip(leaves, grads):
         assert torch.equal(x.grad, g)
     # only what is asked for, and a gradient that comes expanded
     vv = v.clone().requires_grad_()
     plan.attend(q, k, vv, kinds=kinds).sum().backward()
-    assert torch.equal(vv.grad, plan.backward(torch.ones_like(o2), q, k, v, o2, lse, kinds=kinds)[2])
+    assert torch.equal(vv.grad, plan.backward(torch.ones_like(o2), q, k, v, o2, lse, kinds=kinds)[2])   # dv: no delta
 
     def loss(h, x, y, z):
         keep = keep_for_head([S_, T_][h], wl, 1, 11)
@@ -245,9 +258,8 @@ def test_attend_matches_backward_and_differences():
             up[i], down[i] = x[i] + e * u, x[i] - e * u
             slope = (loss(h, *up) - loss(h, *down)) / (2 * e)
             al = allowed_blocks(keep_for_head([S_, T_][h], wl, 1, 11), oracle.layout_slots(h, 4, 6, 8), 64).cuda()
-            _, _, _, bounds = reference(q[0, h], k[0, h], v[0, h], do[0, h], al)
-            # O comes rounded to bf16: delta is off by at most U sum |do o|
-            room = float((bounds[i] * u.abs()).sum()) + 2.0 ** -8 * float((grads[i][0, h].double().abs() * u.abs()).sum())
+            _, _, _, bounds = reference(q[0, h], k[0, h], v[0, h], do[0, h], al, own_o=True)
+            room = 1.1 * float((bounds[i] * u.abs()).sum())
             assert abs(slope - float((grads[i][0, h].double() * u).sum())) <= room
 
 
@@ -425,6 +437,10 @@ def test_refusals():
         vsa.SparseAttention(1, 2, 4, 8, 8, 64, 64, select="given").backward(q, q, q, q, q, lse, kinds=kinds)
     with pytest.raises(ValueError, match="with_grad"):
         vsa.SparseAttention(1, 2, 4, 8, 8, 64, 64, select="given").attend(q, q, q, kinds=kinds)
+    with pytest.raises(ValueError, match="o_lo"):
+        vsa.SparseAttention(1, 2, 4, 8, 8, 64, 64, select="given")(q, q, q, kinds=kinds, o_lo=q)
+    with pytest.raises(ValueError, match="contiguous"):
+        plan.backward(q, q, q, q, q, lse, kinds=kinds, o_lo=q.float())
     with pytest.raises(ValueError, match="no gradient"):
         vsa.SparseAttention(1, 2, 4, 8, 8, 128, 128, select="given", qk_fp8=True, with_grad=True)
     # a host address is refused before any launch

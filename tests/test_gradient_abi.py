@@ -16,7 +16,7 @@ s = ctypes.c_void_p(0)
 
 
 def _set(**kw):
-    return _lib.QKVOGrad(**{**{n: FAKE for n, _ in _lib.QKVOGrad._fields_}, "d_lse": None, **kw})
+    return _lib.QKVOGrad(**{**{n: FAKE for n, _ in _lib.QKVOGrad._fields_}, "d_lse": None, "o_lo": None, **kw})
 
 
 def _lists(nat, perm, shape, ws_bytes, max_kv=4, scale=0.0, ws=FAKE):
@@ -29,7 +29,7 @@ def test_lists_refused_before_launch():
     need = _lib.vsa_sparse_attn_bwd_workspace_size(shape)
     assert need == 256 + 2 * 4 * 64 * 8                    # bitsets (2*4 words, 256-aligned), two terms a row
     for name, _ in _lib.QKVOGrad._fields_:
-        if name != "d_lse":
+        if name not in ("d_lse", "o_lo"):
             assert _lists(_set(**{name: None}), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
             assert _lists(_set(), _set(**{name: None}), shape, need) == _lib.VSA_ERR_INVALID_ARG
             assert _lists(_set(**{name: FAKE + 4}), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
@@ -135,3 +135,24 @@ def test_norm_refused_before_launch():
     for d in (1, 64, 100, 1536, 16384):                                  # and at most a few MB a kernel's width
         for dtype in (0, 1):
             assert 4 * d <= size(_lib.make_norm_shape(1, 1, 1 << 20, d), dtype) <= 148 * 512 * 32 * 4 + 256
+
+
+def test_train_call_refused_before_launch():
+    shape, params = _lib.make_shape(1, 2, 4, 8, 8, 128, 128), _lib.make_params(0, 0)
+
+    def call(io=(FAKE, FAKE, FAKE, FAKE, FAKE), o_lo=FAKE + 64, p=params, ws_bytes=1 << 40):
+        q = _lib.QKVO(*io)
+        return _lib.lib.vsa_attention_train(ctypes.byref(q), o_lo, 1, ctypes.byref(shape), ctypes.byref(p), 1, FAKE, None, FAKE, ws_bytes,
+                                            FAKE, s)
+
+    need = _lib.vsa_attention_train_workspace_size(shape, params, 1, 1)
+    assert need >= _lib.vsa_attention_workspace_size(shape, params, 1, 1) + 2 * 256 * 128 * 2
+    assert _lib.vsa_attention_train_workspace_size(shape, _lib.make_params(0, 0, qk_fp8=True), 1, 1) == 0
+    assert call(o_lo=None) == _lib.VSA_ERR_INVALID_ARG and call(o_lo=FAKE + 4) == _lib.VSA_ERR_INVALID_ARG
+    assert call(o_lo=FAKE) == _lib.VSA_ERR_INVALID_ARG                              # o itself
+    assert call(io=(FAKE, FAKE, FAKE, FAKE, None)) == _lib.VSA_ERR_INVALID_ARG      # no lse
+    assert call(io=(FAKE, None, FAKE, FAKE, FAKE)) == _lib.VSA_ERR_INVALID_ARG
+    assert call(p=_lib.make_params(0, 0, qk_fp8=True)) == _lib.VSA_ERR_UNSUPPORTED
+    if torch.cuda.is_available():                                                   # the workspace is looked at after the pointer
+        return
+    assert call() == _lib.VSA_ERR_INVALID_ARG
