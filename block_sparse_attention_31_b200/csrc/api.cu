@@ -560,9 +560,9 @@ vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo* natural, const uint8_t* d
 // ---------------------------------------------------------------------------------------
 // Gradient of the attention
 // ---------------------------------------------------------------------------------------
-// Workspace of vsa_sparse_attn_bwd: one bitset and two terms per row of every query block.
+// Workspace of vsa_sparse_attn_bwd: one bitset of every query block, two terms and the sum of dS of every row.
 struct BwdLayout {
-  size_t off_bits, off_terms, bytes;
+  size_t off_bits, off_terms, off_target, bytes;
 };
 
 static BwdLayout bwd_layout(const Geom& g, int BH) {
@@ -570,7 +570,8 @@ static BwdLayout bwd_layout(const Geom& g, int BH) {
   const size_t rows = static_cast<size_t>(BH) * g.nblk;
   L.off_bits = 0;
   L.off_terms = align256(rows * ((g.nblk + 31) / 32) * 4);
-  L.bytes = L.off_terms + align256(rows * g.block * 8);
+  L.off_target = L.off_terms + align256(rows * g.block * 8);
+  L.bytes = L.off_target + align256(rows * g.block * 4);
   return L;
 }
 
@@ -618,18 +619,21 @@ static vsa_status sparse_attn_bwd_impl(const vsa_qkvo_grad* natural, const vsa_q
   p.kv_cnt = d_kv_cnt;
   p.o_nat = rows->o;
   p.do_nat = rows->d_o;
-  p.lo_nat = rows->o_lo;
   p.lse_nat = rows->lse;
   p.dlse_nat = rows->d_lse;
   if (permuted != nullptr) {
     p.o_perm = permuted->o;
     p.do_perm = permuted->d_o;
-    p.lo_perm = permuted->o_lo;
     p.lse_perm = permuted->lse;
     p.dlse_perm = permuted->d_lse;
   }
   p.rbits = reinterpret_cast<uint32_t*>(w + L.off_bits);
   p.terms = reinterpret_cast<float*>(w + L.off_terms);
+  // with O's rounding errors from every set that is read, delta is exact
+  const bool exact = rows->o_lo != nullptr && (by_token || permuted == nullptr || permuted->o_lo != nullptr);
+  p.lo_nat = exact ? rows->o_lo : nullptr;
+  p.lo_perm = exact && permuted != nullptr ? permuted->o_lo : nullptr;
+  p.target = exact ? reinterpret_cast<float*>(w + L.off_target) : nullptr;
   p.err = d_err;
   p.BH = BH;
   p.d = d;
@@ -643,6 +647,8 @@ static vsa_status sparse_attn_bwd_impl(const vsa_qkvo_grad* natural, const vsa_q
   a.kinds = d_kind;
   a.rbits = p.rbits;
   a.terms = p.terms;
+  a.target = p.target;
+  a.exact = exact;
   a.err = d_err;
   a.nat_dq = natural->dq;
   a.nat_dk = natural->dk;

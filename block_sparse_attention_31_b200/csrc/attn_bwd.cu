@@ -15,16 +15,22 @@
 //               bitset) and accumulate dV and dK in TMEM.  S^T = K Q^T and dP^T = V dO^T have the
 //               keys as TMEM lanes, so that P^T and dS^T are written over them as packed bf16 and
 //               read from TMEM as the A operands of dV += P^T dO and dK += dS^T Q.
-//   query CTAs  own one query block: they walk its kept key blocks and accumulate dQ; S = Q K^T
-//               and dP = dO V^T have the queries as lanes, dS is written over S.
+//   query CTAs  own one query block: they walk its kept key blocks and accumulate dQ += dS K and the
+//               row's mean key m += P K; S = Q K^T and dP = dO V^T have the queries as lanes.
 //
-// S and dP are computed twice (7 products instead of 5) so that every gradient has one owner:
-// no atomics, no fp32 copy of dQ in memory, the same bits on every run.
+// S and dP are computed twice so that every gradient has one owner: no atomics, no fp32 copy of dQ in
+// memory, the same bits on every run.
+//
+// Why the mean key.  The sum of dS over a row is known (d_lse; 0 without one), and what all of a row's keys
+// have in common drops out of dQ.  It does not drop out of errors: rounding dS to bf16, and a delta that is
+// off, leave a sum e that adds e m to dQ.  The query CTA adds up e in fp32 and takes e m off again.  Without
+// it dQ measured 0.0043 (2-norm, relative) from 64 bits on keys with a common part twice their own size,
+// against 0.0024 with it; the eighth product costs 9% of the time.
 //
 // Each CTA: 384 threads in three warpgroups (registers rebalanced as in the forward kernel).
 //   warps 0-3 / 4-7  one lane (row of S) per thread, the first / second half of its columns:
-//                    p = exp2(s * scale * log2 e - lse * log2 e) in fp32, packed to bf16 for the
-//                    dV product, kept in registers in fp32 for dS = p * (dP - delta)
+//                    p = exp2(s * scale * log2 e - lse * log2 e) in fp32, packed to bf16 for its
+//                    product, kept in registers in fp32 for dS = p * (dP - delta)
 //   warp 8 / 10      TMA producers of the two rings (X: Q or K with the rows' terms; Y: dO or V)
 //   warp 9           the tcgen05 issuer (one lane); owns TMEM
 // P and dS are rounded to bf16 because both operands of the tensor product have one type; every
@@ -50,7 +56,7 @@ constexpr int kMaxSmem = 232448;
 constexpr int kRegsSoftmax = 208, kRegsCtl = 88;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl == 384 * 168, "register split must equal the launch total");
 
-template <int D, int BN, bool kKey>
+template <int D, int BN>
 struct BwdCfg {
   // Ring stages of X (Q or K) and Y (dO or V) and of the rows' terms.  A tile takes about 1500 cycles to
   // arrive; with a spare stage of each no product waits for it.  The spare X stage is given up where the
@@ -71,10 +77,9 @@ struct BwdCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_BITS = OFF_MISC + 16;
   // TMEM columns.  S; dP with P and dS (packed bf16) written over it once it has been read: each half
-  // of the columns holds its threads' dP, then P (key CTA only) and dS.  Behind them dV and dK, or dQ
-  // and the query block's Q and dO as A operands.
-  static constexpr int TM_S = 0, TM_DP = BN, TM_DS = kKey ? BN / 4 : 0, TM_ACC = 2 * BN;
-  static constexpr int TM_Q = TM_ACC + D, TM_DO = TM_Q + D / 2;
+  // of the columns holds its threads' dP, then P and dS.  Behind them the products with P (dV, or the mean
+  // key) and with dS (dK or dQ).
+  static constexpr int TM_S = 0, TM_DP = BN, TM_P = TM_DP, TM_DS = TM_DP + BN / 4, TM_ACC_P = 2 * BN, TM_ACC_DS = 2 * BN + D;
   static constexpr int TM_COLS = 2 * BN + 2 * D <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_S = idesc_bf16_f32(kBM, BN, false, false);
   static constexpr uint32_t IDESC_G = idesc_bf16_f32(kBM, D, false, true);
@@ -93,7 +98,7 @@ enum {
   B_S = 14,        // S (dP) is in TMEM
   B_DP = 15,
   B_SREAD = 16,    // S has been read into registers
-  B_P = 17,        // key CTA: P is written; query CTA, once: Q and dO are in TMEM
+  B_P = 17,        // P is written
   B_DS = 18,       // dS is written
   B_FINAL = 19,
 };
@@ -127,6 +132,10 @@ __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
   return pack_bf16x2(x0, x1);
 }
 
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t x) {
+  return f2_make(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
 // N consecutive TMEM columns of this thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
@@ -136,14 +145,21 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
   reg_fence<N>(r);
 }
 
-// One lane's D (or D/2) accumulator columns -> bf16 rows of the swizzled staging tile.
-template <int BN, int COLS>
-__device__ __forceinline__ void stage_rows(uint8_t* stage, uint32_t taddr, int col0, int row, bool live, bool have,
-                                           float scale) {
+// One lane's COLS accumulator columns (less `off` times those at `other`) -> a bf16 row of the swizzled staging
+// tile.
+template <int BN, int COLS, bool kOther>
+__device__ __forceinline__ void stage_rows(uint8_t* stage, uint32_t taddr, uint32_t other, float off, int col0, int row,
+                                           bool live, bool have, float scale) {
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     float o[32];
     tmem_ld32(taddr + c * 32, o);
+    if constexpr (kOther) {
+      float m[32];
+      tmem_ld32(other + c * 32, m);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = fmaf(-off, m[x], o[x]);
+    }
 #pragma unroll
     for (int x = 0; x < 32; ++x) o[x] = have && live ? o[x] * scale : 0.f;
     if (row < BN) {
@@ -166,7 +182,7 @@ __device__ __forceinline__ void stage_rows(uint8_t* stage, uint32_t taddr, int c
 template <int D, int BN, bool kKey>
 __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, const BwdArgs& a, int bh, int blk,
                                         uint8_t* smem) {
-  using C = BwdCfg<D, BN, kKey>;
+  using C = BwdCfg<D, BN>;
   constexpr int H = BN / 2;  // columns per thread
   const uint32_t sbase = smem_u32(smem);
   const int nx = a.nx;
@@ -350,18 +366,14 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
           if (ok && !mbar_wait(bar(b), parity, abort_flag, a.err)) ok = false;
           return ok;
         };
-        // D[lanes, BN] = A * ring tile^T, A from shared memory (key CTA) or TMEM (query CTA)
-        auto product = [&](uint32_t d_tm, uint64_t a_sm, uint32_t a_tm, uint64_t db) {
+        // D[lanes, BN] = resident tile * ring tile^T
+        auto product = [&](uint32_t d_tm, uint64_t da, uint64_t db) {
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t b = db + static_cast<uint64_t>(((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16);
-            if constexpr (kKey)
-              tc_mma_ss(d_tm, a_sm + static_cast<uint64_t>(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) / 16), b,
-                        C::IDESC_S, kk > 0 ? 1u : 0u);
-            else
-              tc_mma_ts(d_tm, a_tm + kk * 8, b, C::IDESC_S, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ss(d_tm, da + static_cast<uint64_t>(((kk >> 2) * (kBM * 128) + (kk & 3) * 32) / 16),
+                      db + static_cast<uint64_t>(((kk >> 2) * (BN * 128) + (kk & 3) * 32) / 16), C::IDESC_S,
+                      kk > 0 ? 1u : 0u);
         };
         // acc[lanes, D] += packed bf16 (TMEM, two halves) * ring tile
         auto accumulate = [&](uint32_t d_tm, uint32_t a_tm, uint64_t db, bool first) {
@@ -379,7 +391,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
             tp ^= ts == 0;
           }
           if (!first && !wait(B_SREAD, parity)) return;
-          product(tmem + C::TM_S, da0, tmem + C::TM_Q, dxk + xs * kStage);
+          product(tmem + C::TM_S, da0, dxk + xs * kStage);
           tc_commit(bar(B_S));
           if (++xs == nx) {
             xs = 0;
@@ -388,7 +400,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
         };
         auto next_dp = [&]() {
           if (!wait(B_FULL_Y + ys, yp)) return;
-          product(tmem + C::TM_DP, da1, tmem + C::TM_DO, dyk + ys * kStage);
+          product(tmem + C::TM_DP, da1, dyk + ys * kStage);
           tc_commit(bar(B_DP));
           if (!kKey) tc_commit(bar(B_REL_Y + ys));
           if (++ys == C::NY) {
@@ -399,24 +411,20 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
         // S of the next block is issued as soon as S has been read, and runs under the exponentials.
         // Products of one thread complete in order, so B_DP of a block says that the products of the
         // block before have read P and dS, which then may be written over dP.
-        if (kKey) {
-          wait(B_A0, 0);
-          wait(B_A1, 0);
-        } else {
-          wait(B_P, 0);
-        }
+        wait(B_A0, 0);
+        wait(B_A1, 0);
         if (ok) next_s(true, 0);
         if (ok) next_dp();
         for (int n = 0; ok && n < U; ++n) {
           if (n + 1 < U) next_s(false, n & 1);
-          if constexpr (kKey) {
-            if (!wait(B_P, n & 1)) break;
-            accumulate(tmem + C::TM_ACC, tmem + C::TM_DP, dym + yr * kStage, n == 0);
+          if (!wait(B_P, n & 1)) break;
+          accumulate(tmem + C::TM_ACC_P, tmem + C::TM_P, kKey ? dym + yr * kStage : dxm + xr * kStage, n == 0);
+          if (kKey) {
             tc_commit(bar(B_REL_Y + yr));
             if (++yr == C::NY) yr = 0;
           }
           if (!wait(B_DS, n & 1)) break;
-          accumulate(tmem + C::TM_ACC + (kKey ? D : 0), tmem + C::TM_DP + C::TM_DS, dxm + xr * kStage, n == 0);
+          accumulate(tmem + C::TM_ACC_DS, tmem + C::TM_DS, dxm + xr * kStage, n == 0);
           tc_commit(bar(B_REL_X + xr));
           if (++xr == nx) xr = 0;
           if (n + 1 < U) next_dp();
@@ -453,26 +461,14 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
     };
-    if (!kKey && U > 0) {
-      // Q (warps 0-3) and dO (4-7) into TMEM, packed as they are: as A operands read from there they leave
-      // the shared memory's bandwidth to the ring tiles
-      wait(half ? B_A1 : B_A0, 0);
-      const uint8_t* tile = smem + (half ? C::OFF_A1 : C::OFF_A0);
-#pragma unroll
-      for (int c = 0; c < C::PANELS; ++c) {
-        uint32_t r[32];
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(r + ch * 4) =
-              *reinterpret_cast<const uint4*>(tile + c * (kBM * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
-        tmem_st_cols<32>(t_lane + (half ? C::TM_DO : C::TM_Q) + c * 32, r);
-      }
-      arrive(B_P);
-    }
     BitWalk walk(bits);
     // A wait costs 100 to 200 cycles even when its barrier has completed (the tensor core keeps the
     // shared memory busy), so the barriers are tested ahead, under arithmetic.
     bool s_in = false, dp_in = false;
+    // query CTA: the sum of the row's rounded dS, less that of the unrounded (or, with an exact delta, than
+    // what it has to be)
+    uint64_t off = 0ull;
+    const uint64_t minus = a.exact ? f2_make(0.f, 0.f) : f2_make(-1.f, -1.f);
     for (int n = 0; n < U; ++n) {
       const int b = walk.next();
       if (!__all_sync(0xffffffffu, ok)) break;  // after a wait that gave up the rest runs on without waiting
@@ -509,7 +505,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
       tc_fence_after();
       uint32_t r[H];
       tmem_ld_cols<H>(t_dp, r);
-      if constexpr (kKey) {
+      {
         uint32_t pk[H / 2];
 #pragma unroll
         for (int c = 0; c < H / 2; ++c) pk[c] = pack_pair(p[c]);
@@ -521,12 +517,17 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
 #pragma unroll
       for (int c = 0; c < H / 2; c += 2) {
         const ulonglong2 nd = kKey ? terms[BN / 4 + c / 2] : make_ulonglong2(nd_row, nd_row);
-        pk[c] =
-            pack_pair(f2_mul(p[c], f2_add(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), nd.x)));
-        pk[c + 1] = pack_pair(
-            f2_mul(p[c + 1], f2_add(f2_make(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3])), nd.y)));
+        const uint64_t d0 = f2_mul(p[c], f2_add(f2_make(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1])), nd.x));
+        const uint64_t d1 =
+            f2_mul(p[c + 1], f2_add(f2_make(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3])), nd.y));
+        pk[c] = pack_pair(d0);
+        pk[c + 1] = pack_pair(d1);
+        if constexpr (!kKey) {
+          off = f2_add(off, f2_fma(d0, minus, unpack_pair(pk[c])));
+          off = f2_add(off, f2_fma(d1, minus, unpack_pair(pk[c + 1])));
+        }
       }
-      tmem_st_cols<H / 2>(t_dp + (kKey ? H / 2 : 0), pk);
+      tmem_st_cols<H / 2>(t_dp + H / 2, pk);
       arrive(B_DS);
     }
     ok = __all_sync(0xffffffffu, ok);
@@ -542,20 +543,29 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
     const bool have = ok && U > 0;
     if constexpr (kKey) {
       // warps 0-3 write dV over V's tile, warps 4-7 dK over K's
-      const int off = half ? C::OFF_A0 : C::OFF_A1;
-      stage_rows<BN, D>(smem + off, t_lane + C::TM_ACC + half * D, 0, row, live, have, half ? a.scale : 1.f);
+      const int tile = half ? C::OFF_A0 : C::OFF_A1;
+      stage_rows<BN, D, false>(smem + tile, t_lane + (half ? C::TM_ACC_DS : C::TM_ACC_P), 0, 0.f, 0, row, live, have,
+                               half ? a.scale : 1.f);
       fence_proxy_async_smem();
       named_barrier_sync(1 + half, 128);
       if (quad == 2 && lane == 0) {
 #pragma unroll
         for (int c = 0; c < C::PANELS; ++c)
-          tma_store_3d(half ? &m->dk : &m->dv, sbase + off + c * BN * 128, c * 64, blk * BN, bh);
+          tma_store_3d(half ? &m->dk : &m->dv, sbase + tile + c * BN * 128, c * 64, blk * BN, bh);
         tma_store_commit();
         tma_store_wait_read();
       }
     } else {
-      stage_rows<BN, D / 2>(smem + C::OFF_A0, t_lane + C::TM_ACC + half * (D / 2), half * (D / 2), row, live, have,
-                            a.scale);
+      // the row's two threads add up how far its sum of dS is off
+      float* both = reinterpret_cast<float*>(smem + rest);  // the terms' ring, which only key CTAs use
+      float o0, o1;
+      f2_split(off, o0, o1);
+      both[half * kBM + row] = o0 + o1;
+      named_barrier_sync(1, 256);
+      float sum = both[row] + both[kBM + row];
+      if (a.exact && row < BN) sum -= a.target[(static_cast<size_t>(bh) * g.nblk + blk) * BN + row];
+      stage_rows<BN, D / 2, true>(smem + C::OFF_A0, t_lane + C::TM_ACC_DS + half * (D / 2),
+                                  t_lane + C::TM_ACC_P + half * (D / 2), sum, half * (D / 2), row, live, have, a.scale);
       fence_proxy_async_smem();
       named_barrier_sync(1, 256);
       if (warp == 2 && lane == 0) {
@@ -613,7 +623,8 @@ __device__ __forceinline__ uint4 load8(const void* p, size_t at, bool f32) {
 // CTAs [0, mask_ctas): one warp per query block checks its list (ascending, in range, count within
 // max_kv) and writes it as bits; a bad list sets the error bit and becomes empty.
 // The others: d / 16 threads per slot of a head's padded rows, kPrepRows slots at a time so that every thread has
-// eight 16-byte loads in flight; the two terms of each slot's row.
+// eight 16-byte loads in flight; the two terms of each slot's row.  kLo: O has its rounding errors beside it.
+template <bool kLo>
 __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a) {
   const Geom& g = a.g;
   pdl_launch_dependents();
@@ -656,7 +667,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
   const long long first = static_cast<long long>(blockIdx.x - a.mask_ctas) * (groups * kPrepRows) + threadIdx.x / tpr;
   const long long all = static_cast<long long>(a.BH) * slots;
   const int c = threadIdx.x % tpr;
-  uint4 o[kPrepRows][2], go[kPrepRows][2], lo[kPrepRows][2];
+  uint4 o[kPrepRows][2], go[kPrepRows][2], lo[kLo ? kPrepRows : 1][2];
   float lse[kPrepRows], dlse[kPrepRows];
   bool has[kPrepRows];
 #pragma unroll
@@ -679,8 +690,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
     for (int j = 0; j < 2; ++j) {
       o[r][j] = load8(po, row * a.d + (j * tpr + c) * 8, a.f32);
       go[r][j] = load8(pg, row * a.d + (j * tpr + c) * 8, a.f32);
-      lo[r][j] = make_uint4(0, 0, 0, 0);
-      if (pl != nullptr) lo[r][j] = load8(pl, row * a.d + (j * tpr + c) * 8, a.f32);
+      if constexpr (kLo) lo[r][j] = load8(pl, row * a.d + (j * tpr + c) * 8, a.f32);
     }
     lse[r] = (perm ? a.lse_perm : a.lse_nat)[row];
     dlse[r] = 0.f;
@@ -688,8 +698,8 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
   }
 #pragma unroll
   for (int r = 0; r < kPrepRows; ++r) {
-    float delta = (dot8(o[r][0], go[r][0]) + dot8(o[r][1], go[r][1])) +
-                  (dot8(lo[r][0], go[r][0]) + dot8(lo[r][1], go[r][1]));
+    float delta = dot8(o[r][0], go[r][0]) + dot8(o[r][1], go[r][1]);
+    if constexpr (kLo) delta += dot8(lo[r][0], go[r][0]) + dot8(lo[r][1], go[r][1]);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1)
       if (off < tpr) delta += __shfl_xor_sync(0xffffffffu, delta, off);
@@ -699,6 +709,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
       float* t = a.terms + (at / g.block) * (2 * g.block) + at % g.block;  // slots are whole blocks
       t[0] = sees ? -lse[r] * 1.4426950408889634f : -INFINITY;
       t[g.block] = sees ? dlse[r] - delta : 0.f;
+      if constexpr (kLo) a.target[at] = sees ? dlse[r] : 0.f;
     }
   }
 }
@@ -707,7 +718,7 @@ template <int D, int BN>
 cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cudaStream_t stream) {
   auto kern = sparse_attn_bwd_kernel<D, BN>;
   const int nwords = (a.g.nblk + 31) / 32;
-  using C = BwdCfg<D, BN, true>;  // the two kinds of CTA have one layout of shared memory
+  using C = BwdCfg<D, BN>;
   a.nx = C::stages(nwords);
   const int smem = C::smem_bytes(a.nx, nwords);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
@@ -732,7 +743,7 @@ cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cud
 }  // namespace
 
 bool sparse_attn_bwd_fits(const Geom& g, int BH) {
-  using C = BwdCfg<128, 128, true>;
+  using C = BwdCfg<128, 128>;
   return C::smem_bytes(C::NX_MOST - 1, (g.nblk + 31) / 32) <= kMaxSmem &&
          2LL * BH * g.nblk <= 0x7fffffffLL && static_cast<long long>(BH) * g.nblk * g.block / 8 <= 0x7fffffffLL;
 }
@@ -744,7 +755,8 @@ cudaError_t launch_sparse_attn_bwd(const BwdMaps& nat, const BwdMaps& perm, BwdP
   const int rows_per_cta = kPrepThreads / (d / 16) * kPrepRows;
   prep.mask_ctas = static_cast<int>((lists + kPrepThreads / 32 - 1) / (kPrepThreads / 32));
   const long long grid = prep.mask_ctas + (slots + rows_per_cta - 1) / rows_per_cta;
-  bwd_prep_kernel<<<static_cast<unsigned>(grid), kPrepThreads, 0, stream>>>(prep);
+  if (a.exact) bwd_prep_kernel<true><<<static_cast<unsigned>(grid), kPrepThreads, 0, stream>>>(prep);
+  else bwd_prep_kernel<false><<<static_cast<unsigned>(grid), kPrepThreads, 0, stream>>>(prep);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int bn = a.g.block;

@@ -101,6 +101,7 @@ struct BwdPrep {
   const void *lo_nat, *lo_perm;  // O's rounding errors, or null
   const float *lse_nat, *lse_perm, *dlse_nat, *dlse_perm;
   uint32_t* rbits;  // [BH, nblk, ceil(nblk / 32)] kept key blocks of every query block
+  float* target;    // [BH, nblk, block]: what the sum of dS over the row is, or null
   float* terms;     // [BH, nblk, 2, block]: -lse * log2 e (-inf: the row sees nothing), then -delta
   int* err;
   int BH, d, max_kv, has_perm, nat_rows;
@@ -114,10 +115,12 @@ struct BwdArgs {
   const uint8_t* kinds;
   const uint32_t* rbits;
   const float* terms;
+  const float* target;
   int* err;
   void *nat_dq, *nat_dk, *nat_dv;  // zeroed for a head with an invalid kind byte
   int BH, has_perm, nat_rows;
   int nx;                          // ring stages, set by the launcher
+  int exact;                       // delta comes from the unrounded O: the rows' sums of dS are `target`
   float scale, scale_log2;
   Geom g;
 };

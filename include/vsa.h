@@ -390,11 +390,12 @@ typedef struct {
     const float *lse;             /* the forward call's log-sum-exp (required) */
     const float *d_lse;           /* gradient of lse, or NULL */
     void *dq, *dk, *dv;
-    const void *o_lo;             /* what rounding o to bf16 left over (vsa_attention_train), or NULL */
+    const void *o_lo;             /* what rounding o to bf16 left over (vsa_attention_train), or NULL;
+                                     given in every set that is read, or it counts for nothing */
 } vsa_qkvo_grad;
 
 /* Workspace bytes of vsa_sparse_attn_bwd: a bitset of the lists (B*H*nblk*ceil(nblk/32) words)
- * and two fp32 terms per row; 0 for a shape that is invalid or too large. */
+ * and three fp32 terms per row; 0 for a shape that is invalid or too large. */
 VSA_API size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape *shape);
 
 /*
@@ -402,8 +403,10 @@ VSA_API size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape *shape);
  * delta = rowsum(d_o * (o + o_lo)) - d_lse,
  *   dv = P^T d_o,   dS = P * (d_o v^T - delta),   dq = scale dS k,   dk = scale dS^T q.
  * P and dS are rounded to bf16 in front of their tensor products, every sum is fp32, the
- * gradients are bf16.  Each is written by one owner: two runs give the same bits.  delta takes o as it is
- * given: the error of a bf16 o moves a row's dq by that error times its mean key, which o_lo takes away.
+ * gradients are bf16.  Each is written by one owner: two runs give the same bits.  What rounding dS adds to
+ * its sum over a row is taken off dq again.  delta takes o as it is given: the error of a bf16 o moves a
+ * row's dq by that error times the row's mean key.  With o_lo delta is exact, and the sum of dS over a
+ * row is held to what it then is, d_lse (a sixth more time).
  *   natural, permuted   as for vsa_sparse_attn_fwd (permuted may be NULL); bf16; padding slots
  *                       of cube layouts hold finite values, zero as vsa_permute leaves them.
  *                       Every row of a head's layout is written, rows that hold no token or

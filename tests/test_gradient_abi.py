@@ -27,7 +27,7 @@ def _lists(nat, perm, shape, ws_bytes, max_kv=4, scale=0.0, ws=FAKE):
 def test_lists_refused_before_launch():
     shape = _lib.make_shape(1, 2, 4, 8, 8, 64, 64)
     need = _lib.vsa_sparse_attn_bwd_workspace_size(shape)
-    assert need == 256 + 2 * 4 * 64 * 8                    # bitsets (2*4 words, 256-aligned), two terms a row
+    assert need == 256 + 2 * 4 * 64 * 12                   # bitsets (2*4 words, 256-aligned), three terms a row
     for name, _ in _lib.QKVOGrad._fields_:
         if name not in ("d_lse", "o_lo"):
             assert _lists(_set(**{name: None}), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
