@@ -206,6 +206,7 @@ def test_call_pattern_heads(F, Hl, Wl, d, block, dtype):
                                    layout_in_kernel=layout)
         _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, d_lse=d_lse)
         _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, lo=True)
+        _plan_case(plan, wl, [S_, T_], q, k, v, do, kinds=kinds, d_lse=d_lse, lo=True)
 
 
 @pytest.mark.parametrize("F,Hl,Wl,topk", [(5, 5, 9, 3), (9, 9, 17, 4), (4, 4, 8, 2)])
