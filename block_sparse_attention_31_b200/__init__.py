@@ -213,7 +213,7 @@ class SparseAttention(_HostPipelined):
             if self.ws_bwd_bytes == 0:
                 raise VsaError(_lib.VSA_ERR_UNSUPPORTED, "vsa_attention_bwd_workspace_size")
             self.ws_bwd = torch.empty(self.ws_bwd_bytes, dtype=torch.uint8, device=self.device)
-            self.kinds_bwd = torch.full((B * H,), VSA_CUBE, dtype=torch.uint8, device=self.device)
+            self.kinds_bwd = torch.full((B * H,), VSA_CUBE, dtype=torch.uint8, device=self.device)  # or given ones, cast
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None, kinds: Optional[torch.Tensor] = None, stream=None,
@@ -268,9 +268,12 @@ class SparseAttention(_HostPipelined):
                     raise ValueError("backward needs the kinds of the call")
                 if kinds.numel() != self.B * self.H:
                     raise ValueError(f"{self.B * self.H} kinds expected")
-                self.kinds_bwd.copy_(kinds.reshape(-1).to(torch.uint8))
+                if kinds.dtype != torch.uint8 or kinds.device != self.device or not kinds.is_contiguous():
+                    kinds = self.kinds_bwd.copy_(kinds.reshape(-1).to(torch.uint8))
+            else:
+                kinds = self.kinds_bwd  # every head is a cube head
             vsa_attention_bwd(qkvo_grad(q, k, v, o, d_o, lse, *out, d_lse=d_lse, o_lo=o_lo), _DTYPE[self.dtype], self.shape,
-                              self.params, self.kinds_bwd, self.ws_bwd, self.ws_bwd_bytes, self.err)
+                              self.params, kinds, self.ws_bwd, self.ws_bwd_bytes, self.err)
         return tuple(out)
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kinds: Optional[torch.Tensor] = None):

@@ -501,17 +501,15 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
               exp2_pair(f2_fma(f2_make(__uint_as_float(r[2 * c + 2]), __uint_as_float(r[2 * c + 3])), sl2, nl.y));
         }
       }
+      uint32_t pp[H / 2];  // packed under the exponentials, which leave the issue slots free
+#pragma unroll
+      for (int c = 0; c < H / 2; ++c) pp[c] = pack_pair(p[c]);
       if (!__all_sync(0xffffffffu, dp_in)) wait(B_DP, n & 1);
       tc_fence_after();
       uint32_t r[H];
       tmem_ld_cols<H>(t_dp, r);
-      {
-        uint32_t pk[H / 2];
-#pragma unroll
-        for (int c = 0; c < H / 2; ++c) pk[c] = pack_pair(p[c]);
-        tmem_st_cols<H / 2>(t_dp, pk);
-        arrive(B_P);
-      }
+      tmem_st_cols<H / 2>(t_dp, pp);
+      arrive(B_P);
       s_in = n + 1 < U && mbar_test(bar(B_S), (n + 1) & 1);
       uint32_t pk[H / 2];
 #pragma unroll
