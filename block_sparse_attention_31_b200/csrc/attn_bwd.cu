@@ -25,13 +25,22 @@
 // have in common drops out of dQ.  It does not drop out of errors: rounding dS to bf16, and a delta that is
 // off, leave a sum e that adds e m to dQ.  The query CTA adds up e in fp32 and takes e m off again.  Without
 // it dQ measured 0.0043 (2-norm, relative) from 64 bits on keys with a common part twice their own size,
-// against 0.0024 with it; the eighth product costs 9% of the time.
+// against 0.0024 with it; the eighth product costs 0.4 of 3.7 ms (12 heads x 32760 rows, d 128, 21% kept).
+// A block's unweighted mean key instead, one K = 16 step, was faster by 0.1 ms but left 0.0036 to 0.0041.
+//
+// What bounds it.  Executed products run at 1500 TFLOP/s there (0.91 of cuBLAS's burst; back to back the power cap
+// holds both to the same 0.9 of the sustained rate).  A key block's loop takes 2500 cycles for 2048 of
+// tensor time: the threads' chain S -> exponentials (MUFU, 1024) -> dP -> dS is the longer one.  What made it so short:
+// S is freed as soon as it has been read, so that the next block's S runs under the exponentials; P and dS go over
+// dP; barriers are tested ahead; the issuing lane is elected, which lets tcgen05.mma run ahead of it (8 products
+// 770 -> 560 cycles against a branch on lane 0).
 //
 // Each CTA: 384 threads in three warpgroups (registers rebalanced as in the forward kernel).
 //   warps 0-3 / 4-7  one lane (row of S) per thread, the first / second half of its columns:
 //                    p = exp2(s * scale * log2 e - lse * log2 e) in fp32, packed to bf16 for its
 //                    product, kept in registers in fp32 for dS = p * (dP - delta)
-//   warp 8 / 10      TMA producers of the two rings (X: Q or K with the rows' terms; Y: dO or V)
+//   warp 8 / 10      TMA producers of the two rings (X: Q or K; Y: dO or V)
+//   warp 11          bulk copies of the rows' terms (key CTAs)
 //   warp 9           the tcgen05 issuer (one lane); owns TMEM
 // P and dS are rounded to bf16 because both operands of the tensor product have one type; every
 // sum (S, dP, dV, dK, dQ) is held in fp32.

@@ -32,6 +32,12 @@
  *   vsa_scatter_rows    the output back to token order
  *   vsa_semantic_attention  all of them with vsa_sparse_attn_fwd on one stream
  *
+ * Training, and the norm in front of the attention (no counterpart in the pages):
+ *
+ *   vsa_sparse_attn_bwd  gradient of vsa_sparse_attn_fwd on the same lists
+ *   vsa_attention_train, vsa_attention_bwd  the whole call with what its gradient needs, and that gradient
+ *   vsa_rms_norm, vsa_rms_norm_bwd  root-mean-square norm of rows (residual, e4m3 codes) and its gradient
+ *
  * Conventions
  *   - Tensors are [B, H, rows, d] row-major (d fastest), bf16 unless stated otherwise.
  *     A head's buffer holds N rows in natural or frame-major order, or C*V rows in
