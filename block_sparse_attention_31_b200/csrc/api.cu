@@ -581,6 +581,9 @@ static vsa_status check_grad(const vsa_qkvo_grad* t) {
                         static_cast<const void*>(t->dq), static_cast<const void*>(t->dk),
                         static_cast<const void*>(t->dv)})
     if (p == nullptr || !aligned16(p)) return VSA_ERR_INVALID_ARG;
+  if (t->dq == t->dk || t->dq == t->dv || t->dk == t->dv) return VSA_ERR_INVALID_ARG;
+  for (const void* in : {t->q, t->k, t->v, t->o, t->d_o, t->o_lo})  // other CTAs still read them
+    if (in == t->dq || in == t->dk || in == t->dv) return VSA_ERR_INVALID_ARG;
   return VSA_OK;
 }
 

@@ -438,6 +438,8 @@ def test_refusals():
         plan.backward(q, q, q, q, q, lse.double(), kinds=kinds)
     with pytest.raises(ValueError, match="out"):
         plan.backward(q, q, q, q, q, lse, kinds=kinds, out=(q, q))
+    with pytest.raises(vsa.VsaError):
+        plan.backward(q, q, q, q, q, lse, kinds=kinds, out=(q, torch.empty_like(q), torch.empty_like(q)))
     with pytest.raises(ValueError, match="with_grad"):
         vsa.SparseAttention(1, 2, 4, 8, 8, 64, 64, select="given").backward(q, q, q, q, q, lse, kinds=kinds)
     with pytest.raises(ValueError, match="with_grad"):
@@ -454,6 +456,6 @@ def test_refusals():
     idx, cnt = torch.zeros(1, 2, 4, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 2, 4, dtype=torch.int32, device="cuda")
     host = torch.zeros(1, 2, 256, 64, dtype=torch.bfloat16)
     with pytest.raises(vsa.VsaError) as ex:
-        _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(q, q, q, q, q, lse, q, q, host), None, kinds, idx, cnt, 1, shape, 0.0, ws,
+        _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(q, q, q, q, q, lse, torch.empty_like(q), torch.empty_like(q), host), None, kinds, idx, cnt, 1, shape, 0.0, ws,
                                  ws.numel(), cuda_err())
     assert ex.value.status == _lib.VSA_ERR_INVALID_ARG

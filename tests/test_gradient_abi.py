@@ -16,7 +16,8 @@ s = ctypes.c_void_p(0)
 
 
 def _set(**kw):
-    return _lib.QKVOGrad(**{**{n: FAKE for n, _ in _lib.QKVOGrad._fields_}, "d_lse": None, "o_lo": None, **kw})
+    out = dict(dq=FAKE + 256, dk=FAKE + 512, dv=FAKE + 768)
+    return _lib.QKVOGrad(**{**{n: FAKE for n, _ in _lib.QKVOGrad._fields_}, **out, "d_lse": None, "o_lo": None, **kw})
 
 
 def _lists(nat, perm, shape, ws_bytes, max_kv=4, scale=0.0, ws=FAKE):
@@ -33,6 +34,8 @@ def test_lists_refused_before_launch():
             assert _lists(_set(**{name: None}), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
             assert _lists(_set(), _set(**{name: None}), shape, need) == _lib.VSA_ERR_INVALID_ARG
             assert _lists(_set(**{name: FAKE + 4}), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
+    for kw in (dict(dq=FAKE), dict(dk=FAKE + 256), dict(o_lo=FAKE + 768)):      # gradients over inputs or each other
+        assert _lists(_set(**kw), None, shape, need) == _lib.VSA_ERR_INVALID_ARG
     assert _lists(_set(), None, shape, need - 1) == _lib.VSA_ERR_WORKSPACE
     assert _lists(_set(), None, shape, need, max_kv=0) == _lib.VSA_ERR_INVALID_ARG
     assert _lists(_set(), None, shape, need, scale=-1.0) == _lib.VSA_ERR_INVALID_ARG
