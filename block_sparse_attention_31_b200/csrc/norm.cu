@@ -11,8 +11,8 @@
 // thread has several loads in flight.  At 6.5 TB/s an SM has some 12 instructions for an element, so the
 // arithmetic runs on packed pairs (f32x2) and a thread holds at least 16 elements of a row where it can:
 // what a row costs once (its reduction, root and exponent) is shared by them.  Measured, of the 6.54 TB/s copy:
-// 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 43 us (0.54: the
-// block's maximum stands between its loads and its stores), 32760 rows of 1536 with residual, sum and codes 58.5 us
+// 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 38.7 us (0.60;
+// 43 with a CTA a block, whose maximum stands between its loads and its stores), 32760 rows of 1536 with residual, sum and codes 58.5 us
 // (0.92); gradients 56 us (0.82) and 84 us (0.73).  All arithmetic is fp32; y, sum and
 // dx are rounded once, when they are written, and y is normalised from the sum before its rounding.
 #include <cfloat>
@@ -354,6 +354,91 @@ __global__ void __launch_bounds__(kBlock ? 1024 : TPR != 0 ? 256 : 512) rms_norm
   }
 }
 
+// Rows of 2 * TPR * VEC elements without a residual to codes with one exponent per block: a CTA's rows are a block.
+// The block's maximum stands between its loads and its stores, so persistent CTAs fetch the next block (cp.async, every
+// thread its own 16 bytes at a time into its own slots: no barrier for them) while they work on one.
+template <typename T, int VEC, int TPR, int ROWS>
+__global__ void __launch_bounds__(1024) rms_norm_block_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint4 ahead[];  // [2 stages][ROWS * 2][threads]
+  __shared__ float red[2][32];
+  const int groups = blockDim.x / TPR, g = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const long long items = static_cast<long long>(a.chunks) * a.BH;
+  auto slot = [&](int st, int r, int j) { return ahead + ((st * ROWS + r) * 2 + j) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](long long item, int st) {
+    if (item < items) {
+      const int bh = static_cast<int>(item % a.BH), chunk = static_cast<int>(item / a.BH);
+      const T* x = static_cast<const T*>(a.x) + row_at(a.x_stride, bh / a.H, bh % a.H, 0);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int n = min((chunk * ROWS + r) * groups + g, a.N - 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          cp_async_16(smem_u32(slot(st, r, j)), x + static_cast<size_t>(n) * a.x_stride[2] + (j * TPR + t) * VEC, 16);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(blockIdx.x, 0);
+  int st = 0;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x, st ^= 1) {
+    const int bh = static_cast<int>(item % a.BH), chunk = static_cast<int>(item / a.BH);
+    const int n0 = chunk * ROWS * groups + g;
+    const size_t out_row = static_cast<size_t>(bh) * a.N;
+    fetch(item + gridDim.x, st ^ 1);  // read two barriers ago
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    float s[ROWS][2 * VEC], stat[ROWS], top = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      stat[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        Chunk<T, VEC> c;
+        c.load(reinterpret_cast<const T*>(slot(st, r, j)));
+        c.get(s[r] + j * VEC);
+        stat[r] += v_dot<VEC>(s[r] + j * VEC, s[r] + j * VEC);
+      }
+    }
+    int none = 0;
+    row_reduce<TPR, ROWS, false>(stat, red, none);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int n = n0 + r * groups;
+      stat[r] = rsqrtf(fmaf(stat[r], 1.f / (2 * TPR * VEC), a.eps));
+      if (t == 0 && n < a.N && a.rstd != nullptr) a.rstd[out_row + n] = stat[r];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = (j * TPR + t) * VEC;
+      float w[VEC];
+      weights<VEC>(a, col, w);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int n = n0 + r * groups;
+        float* f = s[r] + j * VEC;
+        v_scale<VEC>(f, stat[r]);
+        v_mul<VEC>(f, w);
+        top = n < a.N ? v_top<VEC>(f, top) : top;
+        if (a.y != nullptr && n < a.N) Chunk<T, VEC>::store(static_cast<T*>(a.y) + (out_row + n) * a.d + col, f);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if ((threadIdx.x & 31) == 0) red[st][threadIdx.x >> 5] = top;
+    __syncthreads();  // the other half of red is written only behind the next one
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, red[st][w]);
+    const int e = e4m3_block_exponent(fminf(top, FLT_MAX));
+    if (threadIdx.x == 0) a.exps[static_cast<size_t>(bh) * a.chunks + chunk] = e;
+    const E4m3Scale scale(e);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int n = n0 + r * groups;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (n < a.N) store_codes<VEC>(a.codes + (out_row + n) * a.d + (j * TPR + t) * VEC, s[r] + j * VEC, scale);
+    }
+  }
+}
+
 // Persistent CTAs walk the chunks; every thread keeps the weights and the dw of its columns in registers, and the
 // CTA's sum goes to one row of the workspace, which rms_norm_dw_kernel adds up in a fixed order (no atomics).
 template <typename T, int VEC, int NV, int TPR, int ROWS>
@@ -558,6 +643,17 @@ cudaError_t launch_norm_t(NormArgs a, cudaStream_t stream) {
     if (!blocks) {
       rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, false><<<gr, threads, 0, stream>>>(a);
       return cudaGetLastError();
+    }
+    if constexpr (H::TPR != 0 && H::TPR <= 16 && H::VEC > 1 && H::NV == 2) {
+      if (a.res == nullptr && a.d == 2 * H::TPR * H::VEC) {
+        auto kern = rms_norm_block_kernel<T, H::VEC, H::TPR, H::ROWS>;
+        const int smem = 2 * H::ROWS * 2 * 16 * threads;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        const long long most = 148 * (1024 / threads);  // 64 registers a thread
+        kern<<<static_cast<unsigned>(grid < most ? grid : most), threads, smem, stream>>>(a);
+        return cudaGetLastError();
+      }
     }
     if constexpr (H::TPR != 0 && (H::NV <= 2 || H::VEC == 1)) {  // rows of 64 or 128
       rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, true><<<gr, threads, 0, stream>>>(a);

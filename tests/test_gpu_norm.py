@@ -103,6 +103,18 @@ def test_block_scales(N, block, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block,d", [(64, 64), (128, 128)])
+def test_more_blocks_than_fit_at_once(block, d, dtype):
+    """CTAs that take several blocks each, some one more than others, heads of unlike sizes beside each other."""
+    N = 1184 * 9 // 4 // 6 * block + 3      # 2664 blocks: 148 SMs hold at most 1184 of 64 rows at once
+    x = _rand(2, N, 3, d, seed=9, dtype=dtype).transpose(1, 2) * torch.tensor([1.0, 1e-3, 1e3], device="cuda").to(dtype)[:, None, None]
+    a = _case(2, 3, N, d, dtype, x, _rand(d, seed=2, dtype=dtype), None, quantize=block)
+    # codes of a block do not depend on the others'
+    b = vsa.RMSNorm(2, 3, block, d, dtype=dtype, quantize=block)(x[:, :, 77 * block:78 * block], _rand(d, seed=2, dtype=dtype))
+    assert torch.equal(a.codes[:, :, 77 * block:78 * block], b.codes) and torch.equal(a.exps[:, :, 77:78], b.exps)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_strided_and_unaligned_rows(dtype):
     """Views: projection, a slice of a fused projection, rows that start off 16 bytes, broadcast rows."""
     B, H, N, d = 2, 3, 45, 64
