@@ -11,7 +11,7 @@
 // thread has several loads in flight.  At 6.5 TB/s an SM has some 12 instructions for an element, so the
 // arithmetic runs on packed pairs (f32x2) and a thread holds at least 16 elements of a row where it can:
 // what a row costs once (its reduction, root and exponent) is shared by them.  Measured, of the 6.54 TB/s copy:
-// 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 38.7 us (0.60;
+// 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 33.5 us (0.69;
 // 43 with a CTA a block, whose maximum stands between its loads and its stores), 32760 rows of 1536 with residual, sum and codes 58.5 us
 // (0.92); gradients 56 us (0.82) and 84 us (0.73).  All arithmetic is fp32; y, sum and
 // dx are rounded once, when they are written, and y is normalised from the sum before its rounding.
@@ -360,13 +360,13 @@ __global__ void __launch_bounds__(kBlock ? 1024 : TPR != 0 ? 256 : 512) rms_norm
 template <typename T, int VEC, int TPR, int ROWS>
 __global__ void __launch_bounds__(1024) rms_norm_block_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint4 ahead[];  // [2 stages][ROWS * 2][threads]
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][32];
   const int groups = blockDim.x / TPR, g = threadIdx.x / TPR, t = threadIdx.x % TPR;
-  const long long items = static_cast<long long>(a.chunks) * a.BH;
+  const unsigned items = static_cast<unsigned>(a.chunks) * a.BH, heads = a.BH;  // below 2^31
   auto slot = [&](int st, int r, int j) { return ahead + ((st * ROWS + r) * 2 + j) * blockDim.x + threadIdx.x; };
-  auto fetch = [&](long long item, int st) {
+  auto fetch = [&](unsigned item, int st) {
     if (item < items) {
-      const int bh = static_cast<int>(item % a.BH), chunk = static_cast<int>(item / a.BH);
+      const int chunk = item / heads, bh = item - chunk * heads;
       const T* x = static_cast<const T*>(a.x) + row_at(a.x_stride, bh / a.H, bh % a.H, 0);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(1024) rms_norm_block_kernel(const NormArgs a) 
   };
   fetch(blockIdx.x, 0);
   int st = 0;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x, st ^= 1) {
-    const int bh = static_cast<int>(item % a.BH), chunk = static_cast<int>(item / a.BH);
+  for (unsigned item = blockIdx.x; item < items; item += gridDim.x, st ^= 1) {
+    const int chunk = item / heads, bh = item - chunk * heads;
     const int n0 = chunk * ROWS * groups + g;
     const size_t out_row = static_cast<size_t>(bh) * a.N;
     fetch(item + gridDim.x, st ^ 1);  // read two barriers ago
@@ -425,7 +425,10 @@ __global__ void __launch_bounds__(1024) rms_norm_block_kernel(const NormArgs a) 
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     if ((threadIdx.x & 31) == 0) red[st][threadIdx.x >> 5] = top;
     __syncthreads();  // the other half of red is written only behind the next one
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, red[st][w]);
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); w += 4) {  // at least 128 threads
+      const float4 m = *reinterpret_cast<const float4*>(&red[st][w]);
+      top = fmax3(fmax3(top, m.x, m.y), m.z, m.w);
+    }
     const int e = e4m3_block_exponent(fminf(top, FLT_MAX));
     if (threadIdx.x == 0) a.exps[static_cast<size_t>(bh) * a.chunks + chunk] = e;
     const E4m3Scale scale(e);
