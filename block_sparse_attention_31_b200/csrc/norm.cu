@@ -13,7 +13,8 @@
 // what a row costs once (its reduction, root and exponent) is shared by them.  Measured, of the 6.54 TB/s copy:
 // 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 33.5 us (0.69;
 // 43 with a CTA a block, whose maximum stands between its loads and its stores), 32760 rows of 1536 with residual, sum and codes 58.5 us
-// (0.92); gradients 56 us (0.82) and 84 us (0.73).  All arithmetic is fp32; y, sum and
+// (0.92); gradients 54.5 us (0.85) and 81.5 us (0.75), 56.5 and
+// 84 without the next chunk's loads under the work on one.  All arithmetic is fp32; y, sum and
 // dx are rounded once, when they are written, and y is normalised from the sum before its rounding.
 #include <cfloat>
 
@@ -444,10 +445,13 @@ __global__ void __launch_bounds__(1024) rms_norm_block_kernel(const NormArgs a) 
 
 // Persistent CTAs walk the chunks; every thread keeps the weights and the dw of its columns in registers, and the
 // CTA's sum goes to one row of the workspace, which rms_norm_dw_kernel adds up in a fixed order (no atomics).
-template <typename T, int VEC, int NV, int TPR, int ROWS>
+// kAhead: the next chunk is fetched (cp.async, every thread its own 16 bytes at a time into its own slots) while one
+// is worked on, and read from shared memory in both passes, which leaves the registers to the columns' sums.
+template <typename T, int VEC, int NV, int TPR, int ROWS, bool kAhead>
 __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 && NV == 4 ? 1024 : 512, TPR != 0 ? 2 : 1)
     rms_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int C = NV * VEC;
+  extern __shared__ __align__(16) uint4 ahead[];  // kAhead: [2 stages][s, dy, d_sum][ROWS][NV][threads]
   __shared__ float red[2 * ROWS][32];
   __shared__ float dw_smem[TPR == 0 ? 1 : C * TPR];
   int buf = 0;
@@ -468,27 +472,58 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
   const bool has_ds = a.d_sum != nullptr;
   const T* dy = static_cast<const T*>(a.dy);
   const T* ds = has_ds ? static_cast<const T*>(a.d_sum) : dy;
-  const long long items = static_cast<long long>(a.n.chunks) * a.n.BH;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int bh = static_cast<int>(item % a.n.BH), chunk = static_cast<int>(item / a.n.BH);
-    const int b = bh / a.n.H, h = bh - b * a.n.H;
-    const int n0 = chunk * groups * ROWS + g;
-    const size_t out_row = static_cast<size_t>(bh) * N;
-    const T* s = static_cast<const T*>(a.n.x) + row_at(a.n.x_stride, b, h, 0);
-    T* dx = static_cast<T*>(a.dx) + row_at(a.n.res_stride, b, h, 0);
-    Chunk<T, VEC> cs[ROWS][NV], cy[ROWS][NV], cd[ROWS][NV];
-    float rstd[ROWS], dot[ROWS];
+  const unsigned heads = a.n.BH, items = static_cast<unsigned>(a.n.chunks) * heads;  // below 2^31
+  Chunk<T, VEC> held[kAhead ? 1 : 3][ROWS][NV];
+  float rstd_next[ROWS], rstd[ROWS], dot[ROWS];
+  int st = 0;
+  auto slot = [&](int stage, int which, int r, int j) {
+    return ahead + (((stage * (has_ds ? 3 : 2) + which) * ROWS + r) * NV + j) * blockDim.x + threadIdx.x;
+  };
+  auto fetch = [&](unsigned item, int stage) {
+    if (item < items) {
+      const int chunk = item / heads, bh = item - chunk * heads;
+      const size_t out_row = static_cast<size_t>(bh) * N;
+      const T* s = static_cast<const T*>(a.n.x) + row_at(a.n.x_stride, bh / a.n.H, bh % a.n.H, 0);
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int n = min(n0 + r * groups, N - 1);
+      for (int r = 0; r < ROWS; ++r) {
+        const int n = min((chunk * ROWS + r) * groups + g, N - 1);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int col = (j * tpr + t) * VEC, at = col < d ? col : 0;
-        cs[r][j].load(s + static_cast<size_t>(n) * a.n.x_stride[2] + at);
-        cy[r][j].load(dy + (out_row + n) * d + at);
-        if (has_ds) cd[r][j].load(ds + (out_row + n) * d + at);
+        for (int j = 0; j < NV; ++j) {
+          const int col = (j * tpr + t) * VEC, at = col < d ? col : 0;
+          const T* from[3] = {s + static_cast<size_t>(n) * a.n.x_stride[2] + at, dy + (out_row + n) * d + at,
+                              ds + (out_row + n) * d + at};
+#pragma unroll
+          for (int which = 0; which < 3; ++which) {
+            if (which == 2 && !has_ds) continue;
+            if constexpr (kAhead) cp_async_16(smem_u32(slot(stage, which, r, j)), from[which], 16);
+            else held[which][r][j].load(from[which]);
+          }
+        }
+        rstd_next[r] = a.n.rstd[out_row + n];
       }
-      rstd[r] = a.n.rstd[out_row + n];
+    }
+    if constexpr (kAhead) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto get = [&](int which, int r, int j, float* f) {
+    if constexpr (kAhead) {
+      Chunk<T, VEC> c;
+      c.load(reinterpret_cast<const T*>(slot(st, which, r, j)));
+      c.get(f);
+    } else {
+      held[which][r][j].get(f);
+    }
+  };
+  if constexpr (kAhead) fetch(blockIdx.x, 0);
+  for (unsigned item = blockIdx.x; item < items; item += gridDim.x) {
+    const int chunk = item / heads, bh = item - chunk * heads;
+    const int n0 = chunk * groups * ROWS + g;
+    T* dx = static_cast<T*>(a.dx) + row_at(a.n.res_stride, bh / a.n.H, bh % a.n.H, 0);
+    if constexpr (!kAhead) fetch(item, 0);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) rstd[r] = rstd_next[r];
+    if constexpr (kAhead) {
+      fetch(item + gridDim.x, st ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -498,8 +533,8 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
       for (int j = 0; j < NV; ++j) {
         const int col = (j * tpr + t) * VEC;
         float xh[VEC], fy[VEC], wt[VEC];
-        cs[r][j].get(xh);
-        cy[r][j].get(fy);
+        get(0, r, j, xh);
+        get(1, r, j, fy);
         if constexpr (!kHoldW) weights<VEC>(a.n, col < d ? col : 0, wt);
         v_scale<VEC>(xh, rstd[r]);
         if (in) v_fma<VEC>(dw + j * VEC, fy, xh);
@@ -518,11 +553,11 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
       for (int j = 0; j < NV; ++j) {
         const int col = (j * tpr + t) * VEC;
         float fs[VEC], fy[VEC], out[VEC], wt[VEC];
-        cs[r][j].get(fs);
-        cy[r][j].get(fy);
+        get(0, r, j, fs);
+        get(1, r, j, fy);
         if constexpr (!kHoldW) weights<VEC>(a.n, col < d ? col : 0, wt);
         if (has_ds) {
-          cd[r][j].get(out);
+          get(2, r, j, out);
         } else {
 #pragma unroll
           for (int i = 0; i < VEC; ++i) out[i] = 0.f;
@@ -534,6 +569,7 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
         if (n < N && col < d) Chunk<T, VEC>::store(dx + static_cast<size_t>(n) * a.n.res_stride[2] + col, out);
       }
     }
+    st ^= 1;
   }
   if (a.partial == nullptr) return;
   float* mine = a.partial + static_cast<size_t>(blockIdx.x) * d;
@@ -680,8 +716,22 @@ cudaError_t launch_norm_bwd_t(NormBwdArgs a, float* dw, cudaStream_t stream) {
     a.n.chunks = static_cast<int>((static_cast<long long>(a.n.N) + rows - 1) / rows);
     const long long items = static_cast<long long>(a.n.chunks) * a.n.BH;
     const int most = bwd_ctas<H>(n), grid = static_cast<int>(items < most ? items : most);
-    rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS><<<grid, threads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    auto launch = [&](auto kern, int smem) {
+      const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (r == cudaSuccess) kern<<<grid, threads, smem, stream>>>(a);
+      return r;
+    };
+    // two stages take at most 192 KB for 512 threads, as many as an SM holds; fp32 rows of over 8192 take more
+    constexpr bool kVec = H::VEC > 1, kLong = sizeof(T) == 4 && H::TPR == 0 && H::NV == 4;
+    if (kVec && threads <= 512) {
+      const int smem = 2 * (a.d_sum != nullptr ? 3 : 2) * H::ROWS * H::NV * 16 * threads;
+      e = launch(rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec>, smem);
+    } else {
+      e = launch(rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec && !kLong>, 0);
+    }
+    if (e != cudaSuccess) return e;
+    e = cudaGetLastError();
     if (e != cudaSuccess || dw == nullptr) return e;
     rms_norm_dw_kernel<<<(a.n.d + 31) / 32, 1024, 0, stream>>>(a.partial, grid, a.n.d, dw);
     return cudaGetLastError();

@@ -207,6 +207,20 @@ def test_backward_heads_and_strides(dtype):
                    _rand(1, 1, 200000, 64, seed=8, dtype=dtype), None)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,N", [(256, 6007), (1000, 3001), (1536, 3001), (2056, 1301), (8200, 331), (16384, 331)])
+def test_backward_many_rows_a_cta(d, N, dtype):
+    """Every way of holding a row with more chunks than CTAs, some CTAs with one more, with and without d_sum."""
+    x, w, dy, ds = (_rand(*sh, seed=d + i, dtype=dtype) for i, sh in enumerate([(1, 1, N, d), (d,), (1, 1, N, d), (1, 1, N, d)]))
+    for d_sum in (None, ds):
+        dx, _ = _backward_case(1, 1, N, d, dtype, x, w, dy, d_sum)
+        few = vsa.RMSNorm(1, 1, 7, d, dtype=dtype, with_grad=True)
+        rstd = _reference(x, w, None, 1e-6)[1].float()[:, :, -7:].clone()
+        last = few.backward(dy[:, :, -7:].clone(), x[:, :, -7:].clone(), rstd, w,
+                             d_sum=None if d_sum is None else d_sum[:, :, -7:].clone())[0]
+        assert torch.equal(dx[:, :, -7:], last)  # a row's gradient does not depend on the others
+
+
 def test_offsets_past_32_bits():
     """More than 2^31 elements: the last rows come out as they do alone, and the first are not touched by them."""
     B, H, N, d = 1, 137, 122500, 128
