@@ -8,12 +8,12 @@ host batches).
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import _lib
+from ._lib import _on
 from ._lib import (VSA_BF16, VSA_CUBE, VSA_F32, VSA_SELECT_CUBE, VSA_SELECT_GIVEN, VSA_SELECT_PROFILE, VSA_SPATIAL,
                    VSA_TEMPORAL, Params, QKVO, Shape, VsaError, make_params, make_shape, qkvo, vsa_attention,
                    vsa_attention_workspace_layout, vsa_attention_workspace_size, vsa_block_order,
@@ -90,29 +90,6 @@ class _HostPipelined:
             timing[1].record(down)
         down.synchronize()
         return outs
-
-
-
-_HERE = contextlib.nullcontext()
-
-
-@contextlib.contextmanager
-def _there(stream, device):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                   else torch.cuda.ExternalStream(int(stream), device=device)):
-                yield
-
-
-def _on(stream, device):
-    """Context in which `device` and `stream` (a torch stream or a raw handle; None: the device's current one)
-    are current, so that what is allocated in it belongs to the stream that uses it."""
-    if stream is None and (device.type != "cuda" or device.index == torch.cuda.current_device()):
-        return _HERE
-    return _there(stream, device)
 
 
 def _no_capture(what: str):
@@ -245,7 +222,7 @@ class SparseAttention(_HostPipelined):
                  lse: torch.Tensor, kinds: Optional[torch.Tensor] = None, d_lse: Optional[torch.Tensor] = None,
                  out: Optional[Sequence[torch.Tensor]] = None, stream=None, o_lo: Optional[torch.Tensor] = None):
         """Gradients (dq, dk, dv) of a call of this plan, from its inputs, its outputs (``o_lo`` among
-        them, where the call filled it) and the gradients of those.  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
+        them, where the call filled it) and the gradients of those (``lse`` and ``d_lse`` with any strides).  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
         where another call comes between); they are not needed for select="cube".  Nothing else of the
         call is kept: the masks are built again.  Asynchronous on ``stream``; can be captured."""
         if not self.with_grad:
@@ -260,9 +237,8 @@ class SparseAttention(_HostPipelined):
                 if t.dtype != self.dtype or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != shape:
                     raise ValueError(f"contiguous {self.dtype} tensors of shape {shape} on {self.device} expected")
             for t in (lse, d_lse):
-                if t is not None and (t.dtype != torch.float32 or t.device != self.device or not t.is_contiguous()
-                                      or tuple(t.shape) != shape[:3]):
-                    raise ValueError(f"lse and d_lse are contiguous float32 tensors of shape {shape[:3]} on {self.device}")
+                if t is not None and (t.dtype != torch.float32 or t.device != self.device or tuple(t.shape) != shape[:3]):
+                    raise ValueError(f"lse and d_lse are float32 tensors of shape {shape[:3]} on {self.device}")
             if self.select != VSA_SELECT_CUBE:
                 if kinds is None:
                     raise ValueError("backward needs the kinds of the call")

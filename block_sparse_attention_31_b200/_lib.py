@@ -6,6 +6,7 @@ library cannot be loaded, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -57,6 +58,7 @@ class QKVO(ctypes.Structure):
 
 
 class QKVOGrad(ctypes.Structure):
+    held = None  # the tensors behind the addresses, by their fields (qkvo_grad)
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "d_o", "lse", "d_lse", "dq", "dk", "dv", "o_lo")]
 
 
@@ -169,6 +171,28 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _there(stream, device):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(int(stream), device=device)):
+                yield
+
+
+def _on(stream, device):
+    """Context in which `device` and `stream` (a torch stream or a raw handle; None: the device's current one)
+    are current, so that what is allocated in it belongs to the stream that uses it."""
+    if device.type != "cuda" or (stream is None and device.index == torch.cuda.current_device()):
+        return _HERE
+    return _there(stream, device)
 
 
 def make_shape(B, H, F, Hl, Wl, d, block, cube=None) -> Shape:
@@ -332,8 +356,37 @@ def vsa_attention(io: QKVO, dtype: int, shape: Shape, params: Params, select: in
 # ---------------------------------------------------------------------------------------
 
 def qkvo_grad(q, k, v, o, d_o, lse, dq, dk, dv, d_lse=None, o_lo=None) -> QKVOGrad:
-    return QKVOGrad(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(d_lse), _ptr(dq), _ptr(dk),
-                    _ptr(dv), _ptr(o_lo))
+    """One set of the gradient's tensors (or addresses).  lse and d_lse may have their rows anywhere, as in rows cut
+    out of longer ones: the calls copy them where they are not whole rows on 16 bytes."""
+    all_ = (q, k, v, o, d_o, lse, d_lse, dq, dk, dv, o_lo)
+    out = QKVOGrad(*(_ptr(t) for t in all_))
+    out.held = {f[0]: t for f, t in zip(QKVOGrad._fields_, all_) if isinstance(t, torch.Tensor)}
+    return out
+
+
+def _on_16_bytes(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy where it is not contiguous or starts off 16 bytes."""
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _whole_rows(s, stream):
+    """The set with lse and d_lse in whole rows on 16 bytes, copied on `stream` where they are not; the second value
+    holds the copies."""
+    copies = {}
+    if s is not None and s.held:
+        for name in ("lse", "d_lse"):
+            t = s.held.get(name)
+            if t is not None and not (t.is_contiguous() and t.data_ptr() % 16 == 0):
+                with _on(stream, t.device):
+                    copies[name] = _on_16_bytes(t)
+    if not copies:
+        return s, copies
+    out = QKVOGrad.from_buffer_copy(s)
+    for name, t in copies.items():
+        setattr(out, name, t.data_ptr())
+    return out, copies
 
 
 def vsa_attention_train_workspace_size(shape: Shape, params: Params, dtype: int, select: int) -> int:
@@ -353,6 +406,8 @@ def vsa_sparse_attn_bwd_workspace_size(shape: Shape) -> int:
 
 def vsa_sparse_attn_bwd(natural: QKVOGrad, permuted, kinds, kv_idx, kv_cnt, max_kv, shape: Shape, scale, ws, ws_bytes,
                         err, stream=None):
+    natural, copies = _whole_rows(natural, stream)
+    permuted, more = _whole_rows(permuted, stream)
     _check(lib.vsa_sparse_attn_bwd(ctypes.byref(natural), ctypes.byref(permuted) if permuted is not None else None,
                                    _ptr(kinds), _ptr(kv_idx), _ptr(kv_cnt), int(max_kv), ctypes.byref(shape),
                                    float(scale), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)),
@@ -364,6 +419,7 @@ def vsa_attention_bwd_workspace_size(shape: Shape, params: Params, dtype: int) -
 
 
 def vsa_attention_bwd(io: QKVOGrad, dtype: int, shape: Shape, params: Params, kinds, ws, ws_bytes, err, stream=None):
+    io, copies = _whole_rows(io, stream)
     _check(lib.vsa_attention_bwd(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
                                  _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention_bwd")
 

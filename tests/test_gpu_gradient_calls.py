@@ -1,0 +1,96 @@
+"""GPU checks of how the gradient and the norm are called: strided and unaligned arguments, streams, threads, unknown
+head kinds, heads of unlike layouts beside each other."""
+import pytest
+import torch
+
+from grad_util import assert_grads, reference
+from parity_util import cuda_err
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import block_sparse_attention_31_b200 as vsa
+    from block_sparse_attention_31_b200 import _lib
+else:
+    vsa = _lib = None
+
+BF, F32 = torch.bfloat16, torch.float32
+S_, T_ = 0, 1
+
+
+def _rand(*shape, seed=0, dtype=BF):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def _small(select="given", dtype=BF, **kw):
+    """A plan of two heads on a ragged grid, its inputs and the gradient of its output."""
+    plan = vsa.SparseAttention(1, 2, 5, 6, 10, 64, 64, dtype=dtype, select=select, w_s=1, w_t=9, with_grad=True, **kw)
+    return (plan, *(_rand(1, 2, 300, 64, seed=s, dtype=dtype) for s in range(4)))
+
+
+def _in_longer_rows(t):
+    """The same values in rows that are one element longer than they are read."""
+    rows = torch.full((*t.shape[:-1], t.shape[-1] + 1), 1e3, device="cuda")
+    rows[..., :-1] = t
+    return rows[..., :-1]
+
+
+def _off_16_bytes(t):
+    flat = torch.empty(t.numel() + 1, device="cuda")
+    flat[1:] = t.flatten()
+    return flat[1:].view(t.shape)
+
+
+def test_log_sum_exp_in_longer_rows():
+    """lse and d_lse cut out of longer rows, flat or per batch, or off 16 bytes: the bits of whole rows."""
+    B, H, N, d = 2, 3, 300, 64
+    shape = _lib.make_shape(B, H, 1, 1, N, d, 64)
+    nb = _lib.vsa_num_blocks(shape)
+    idx = torch.arange(nb, dtype=torch.int32, device="cuda").expand(B, H, nb, nb).contiguous()
+    cnt = torch.full((B, H, nb), nb, dtype=torch.int32, device="cuda")
+    kinds, err = torch.zeros(B * H, dtype=torch.uint8, device="cuda"), cuda_err()
+    q, k, v, do = (_rand(B, H, N, d, seed=s) for s in range(4))
+    o, lse, d_lse = torch.empty_like(q), torch.empty(B, H, N, device="cuda"), _rand(B, H, N, seed=4, dtype=F32)
+    _lib.vsa_sparse_attn_fwd(_lib.qkvo(q, k, v, o, lse), None, kinds, idx, cnt, nb, shape, 0.0, err)
+    ws = torch.empty(_lib.vsa_sparse_attn_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+
+    def run(lse, d_lse, stream=None):
+        grads = [torch.empty_like(q) for _ in range(3)]
+        _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(q, k, v, o, do, lse, *grads, d_lse=d_lse), None, kinds, idx, cnt, nb, shape, 0.0,
+                                 ws, ws.numel(), err, stream)
+        return grads
+
+    want = run(lse, d_lse)
+    # the whole rows are right, to the eye of the element bounds
+    for h in range(H):
+        _, _, ref, bounds = reference(q[1, h], k[1, h], v[1, h], do[1, h], torch.ones(N, N, dtype=torch.bool, device="cuda"), o=o[1, h],
+                                      lse=lse[1, h], d_lse=d_lse[1, h])
+        assert_grads([g[1, h] for g in want], ref, bounds, f"head {h}")
+    flat = _in_longer_rows(lse.view(B * H, N))
+    assert not flat.is_contiguous()
+    for a, b in ((flat, d_lse), (_in_longer_rows(lse), _in_longer_rows(d_lse)), (_off_16_bytes(lse), _off_16_bytes(d_lse)),
+                 (lse.transpose(0, 1).contiguous().transpose(0, 1), d_lse)):
+        for x, y in zip(run(a, b), want):
+            assert torch.equal(x, y)
+    side = torch.cuda.Stream()
+    late = torch.zeros(B * H, N + 1, device="cuda")[:, :-1]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):      # there when the call's own stream comes to it
+        torch.cuda._sleep(100_000_000)
+        late.copy_(flat)
+    got = run(late, d_lse, side)
+    side.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert _lib.vsa_get_device_error(err) == 0
+
+
+def test_call_takes_a_log_sum_exp_in_longer_rows():
+    plan, q, k, v, do = _small()
+    kinds = torch.tensor([S_, T_], dtype=torch.uint8, device="cuda")
+    o, lse = plan(q, k, v, kinds=kinds)
+    d_lse = _rand(*lse.shape, seed=5, dtype=F32)
+    want = plan.backward(do, q, k, v, o, lse, kinds=kinds, d_lse=d_lse)
+    for cut in (_in_longer_rows, _off_16_bytes):
+        for x, y in zip(plan.backward(do, q, k, v, o, cut(lse), kinds=kinds, d_lse=cut(d_lse)), want):
+            assert torch.equal(x, y)
