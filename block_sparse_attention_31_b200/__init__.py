@@ -463,12 +463,16 @@ class RMSNorm:
         return out
 
     def backward(self, dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
-                 d_sum: Optional[torch.Tensor] = None, stream=None):
-        """(dx, d_weight) of a call: s is its x, or its sum where it had a residual; dy and d_sum the gradients of
-        y and of sum.  dx is the residual's gradient too, and has s's order of dimensions where s fills its
+                 d_sum: Optional[torch.Tensor] = None, stream=None, dsum: Optional[torch.Tensor] = None):
+        """(dx, d_weight) of a call: s is its x, or its sum where it had a residual; dy and d_sum (or dsum, another
+        name of it) the gradients of y and of sum.  dx is the residual's gradient too, and has s's order of dimensions where s fills its
         memory (else it is contiguous); d_weight is fp32 (None without a weight).  Asynchronous on ``stream``; can be captured."""
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
+        if dsum is not None:
+            if d_sum is not None:
+                raise ValueError("d_sum and dsum are one argument")
+            d_sum = dsum
         wt = self._weight(weight)
         with _on(stream, self.device):
             dy = self._rows(dy, "dy", dense=True)

@@ -94,3 +94,13 @@ def test_call_takes_a_log_sum_exp_in_longer_rows():
     for cut in (_in_longer_rows, _off_16_bytes):
         for x, y in zip(plan.backward(do, q, k, v, o, cut(lse), kinds=kinds, d_lse=cut(d_lse)), want):
             assert torch.equal(x, y)
+
+
+def test_gradient_of_the_sum_under_either_name():
+    norm = vsa.RMSNorm(1, 2, 50, 64, with_grad=True)
+    x, w, dy, ds = _rand(1, 2, 50, 64, seed=1), _rand(64, seed=2), _rand(1, 2, 50, 64, seed=3), _rand(1, 2, 50, 64, seed=4)
+    rstd = norm(x, w).rstd
+    for a, b in zip(norm.backward(dy, x, rstd, w, dsum=ds), norm.backward(dy, x, rstd, w, d_sum=ds)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="d_sum"):
+        norm.backward(dy, x, rstd, w, d_sum=ds, dsum=ds)
