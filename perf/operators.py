@@ -317,8 +317,6 @@ def prepare(case, seed):
     if not own:
         return s
     import block_sparse_attention_31_b200 as vsa
-    if "lse" in s:
-        s["lse"] = s["lse"].contiguous()  # the calls take whole rows; the plain form cuts them out of longer ones
     if c["op"] in ("norm", "norm_bwd"):
         s["norm"] = vsa.RMSNorm(c["B"], c["H"], c["N"], c["d"], dtype=s["x"].dtype, eps=1e-6, quantize=c.get("block", 0),
                                 with_grad=c["op"] == "norm_bwd")
@@ -351,7 +349,7 @@ def _own(c, s):
             out["y"] = r.y
         return out
     if c["op"] == "norm_bwd":
-        dx, dw = s["norm"].backward(s["dy"], s["x"], s["rstd"], s["w"], d_sum=s["dsum"])
+        dx, dw = s["norm"].backward(s["dy"], s["x"], s["rstd"], s["w"], dsum=s["dsum"])
         return dict(dx=dx, dw=dw)
     shape = (c["B"], c["H"], c["F"] * c["Hl"] * c["Wl"], c["d"])
     q, k, v, do = (s[x].view(shape) for x in ("q", "k", "v", "do"))
