@@ -105,6 +105,27 @@ static bool on_current_device(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+// One buffer of a call.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether every output lies apart from every input and from the other outputs: some CTAs write while others read.
+static bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& x, const Span& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a != 0 && b != 0 && (a <= b ? b - a < x.bytes : a - b < y.bytes);
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* x = o + 1; x != outs.end(); ++x)
+      if (meet(*o, *x)) return false;
+    for (const Span& x : ins)
+      if (meet(*o, x)) return false;
+  }
+  return true;
+}
+
 // Validate the shape and derive the geometry.
 static vsa_status make_geom(const vsa_shape* s, Geom* g) {
   if (s == nullptr || g == nullptr) return VSA_ERR_INVALID_ARG;
@@ -592,6 +613,13 @@ static bool grad_on_device(const vsa_qkvo_grad* t) {
          on_current_device({t->q, t->k, t->v, t->o, t->d_o, t->lse, t->d_lse, t->dq, t->dk, t->dv, t->o_lo});
 }
 
+// The set's gradients (rows of d elements of es bytes) and the workspace apart from what else the set holds.
+static bool grad_apart(const vsa_qkvo_grad* t, size_t rows, int d, int es, const void* ws, size_t ws_bytes) {
+  const size_t n = rows * d * es, l = rows * 4;
+  return apart({{t->dq, n}, {t->dk, n}, {t->dv, n}, {ws, ws_bytes}},
+               {{t->q, n}, {t->k, n}, {t->v, n}, {t->o, n}, {t->d_o, n}, {t->o_lo, n}, {t->lse, l}, {t->d_lse, l}});
+}
+
 static vsa_status encode_bwd_set(BwdMaps* m, const vsa_qkvo_grad* t, const Geom& g, int rows, int BH, int d) {
   const struct {
     CUtensorMap* map;
@@ -683,7 +711,12 @@ vsa_status vsa_sparse_attn_bwd(const vsa_qkvo_grad* natural, const vsa_qkvo_grad
     return VSA_ERR_INVALID_ARG;
   const int BH = shape->B * shape->H;
   if (!sparse_attn_bwd_fits(g, BH)) return VSA_ERR_UNSUPPORTED;
-  if (ws_bytes < bwd_layout(g, BH).bytes) return VSA_ERR_WORKSPACE;
+  const size_t need = bwd_layout(g, BH).bytes;
+  if (ws_bytes < need) return VSA_ERR_WORKSPACE;
+  const size_t perm_rows = static_cast<size_t>(BH) * g.R, nat_rows = permuted != nullptr ? static_cast<size_t>(BH) * g.N : perm_rows;
+  if (!grad_apart(natural, nat_rows, shape->d, 2, ws, need) ||
+      (permuted != nullptr && !grad_apart(permuted, perm_rows, shape->d, 2, ws, need)))
+    return VSA_ERR_INVALID_ARG;
   if (!grad_on_device(natural) || (permuted != nullptr && !grad_on_device(permuted)) ||
       !on_current_device({d_kind, d_kv_idx, d_kv_cnt, ws, d_err}))
     return VSA_ERR_INVALID_ARG;
@@ -1187,11 +1220,14 @@ size_t vsa_attention_train_workspace_size(const vsa_shape* shape, const vsa_para
 vsa_status vsa_attention_train(const vsa_qkvo* io, void* o_lo, vsa_dtype dtype, const vsa_shape* shape,
                                const vsa_params* params, vsa_select select, uint8_t* d_kind, float* d_mse, void* ws,
                                size_t ws_bytes, int* d_err, cudaStream_t stream) {
-  if (o_lo == nullptr || !aligned16(o_lo) || io == nullptr || io->lse == nullptr || o_lo == io->o)
-    return VSA_ERR_INVALID_ARG;
+  if (o_lo == nullptr || !aligned16(o_lo) || io == nullptr || io->lse == nullptr) return VSA_ERR_INVALID_ARG;
   if (params != nullptr && params->qk_fp8 != 0) return VSA_ERR_UNSUPPORTED;
   vsa_status st = check_qkvo(io);
   if (st != VSA_OK) return st;
+  Geom g;
+  if ((st = make_geom(shape, &g)) != VSA_OK) return st;
+  const size_t rows = static_cast<size_t>(shape->B) * shape->H * g.N, n = rows * shape->d * (dtype == VSA_F32 ? 4 : 2);
+  if (!apart({{o_lo, n}}, {{io->q, n}, {io->k, n}, {io->v, n}, {io->o, n}, {io->lse, rows * 4}})) return VSA_ERR_INVALID_ARG;
   if (!on_current_device({o_lo})) return VSA_ERR_INVALID_ARG;
   return attention_impl(io, o_lo, dtype, shape, params, select, d_kind, d_mse, ws, ws_bytes, d_err, stream);
 }
@@ -1251,6 +1287,8 @@ vsa_status vsa_attention_bwd(const vsa_qkvo_grad* io, vsa_dtype dtype, const vsa
   Geom g;
   make_geom(shape, &g);
   const int BH = shape->B * shape->H;
+  if (!grad_apart(io, static_cast<size_t>(BH) * g.N, shape->d, dtype == VSA_F32 ? 4 : 2, ws, L.bytes))
+    return VSA_ERR_INVALID_ARG;
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint32_t* bits = reinterpret_cast<uint32_t*>(w + L.off_bits);
   int32_t* kv_idx = reinterpret_cast<int32_t*>(w + L.off_idx);

@@ -389,7 +389,7 @@ VSA_API vsa_status vsa_attention_workspace_layout(const vsa_shape *shape, const 
  * ------------------------------------------------------------------------------------- */
 
 /* Pointers of one gradient problem, all [B, H, rows, d] or [B, H, rows]; dq, dk and dv are
- * written and overlap no input.  d_lse (the gradient of the log-sum-exp) may be NULL. */
+ * written and overlap neither each other nor an input of the set (VSA_ERR_INVALID_ARG).  d_lse (the gradient of the log-sum-exp) may be NULL. */
 typedef struct {
     const void *q, *k, *v, *o;    /* the forward call's inputs and output */
     const void *d_o;              /* gradient of o */
@@ -435,7 +435,7 @@ VSA_API size_t vsa_attention_train_workspace_size(const vsa_shape *shape, const 
 /*
  * vsa_attention for a call whose gradient is wanted: the same o and lse (required), and o_lo, what the rounding of
  * o to bf16 left over, rounded to bf16 itself.
- *   o_lo     [B, H, N, d] in dtype out, natural order
+ *   o_lo     [B, H, N, d] in dtype out, natural order; overlaps none of io's buffers
  *   ws       vsa_attention_train_workspace_size bytes
  *   the rest as vsa_attention; qk_fp8 returns VSA_ERR_UNSUPPORTED
  */

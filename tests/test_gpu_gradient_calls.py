@@ -104,3 +104,41 @@ def test_gradient_of_the_sum_under_either_name():
         assert torch.equal(a, b)
     with pytest.raises(ValueError, match="d_sum"):
         norm.backward(dy, x, rstd, w, d_sum=ds, dsum=ds)
+
+
+def test_outputs_over_inputs_are_refused():
+    """O's rounding errors over an input of their call, gradients and workspace over a set's buffers, whole or in part."""
+    plan, q, k, v, do = _small()
+    kinds = torch.tensor([S_, T_], dtype=torch.uint8, device="cuda")
+    o, lse, n = torch.empty_like(q), torch.empty(1, 2, 300, device="cuda"), q.numel()
+    for t in (q, k, v, o, lse.view(BF)):
+        both = torch.cat([t.flatten(), torch.zeros(2 * n, dtype=BF, device="cuda")])       # t, then room behind it
+        mine = both[:t.numel()].view(t.shape)
+        args = dict(q=q, k=k, v=v, out=o, lse=lse)
+        name = next(x for x, y in args.items() if y.data_ptr() == t.data_ptr())
+        args[name] = mine.view(F32).view(lse.shape) if name == "lse" else mine
+        last = (t.numel() - 1) // 8 * 8                                                      # the last place on 16 bytes in t
+        for at in (0, 8, last):
+            with pytest.raises(vsa.VsaError) as e:
+                plan(**args, kinds=kinds, o_lo=both[at:at + n].view(q.shape))
+            assert e.value.status == _lib.VSA_ERR_INVALID_ARG
+        behind = -(-t.numel() // 8) * 8
+        plan(**args, kinds=kinds, o_lo=both[behind:behind + n].view(q.shape))
+    plan(q, k, v, out=o, lse=lse, kinds=kinds)
+    room = torch.zeros(8 * n, dtype=BF, device="cuda")
+    part = lambda at: room[at:at + n].view(q.shape)  # noqa: E731
+    part(0).copy_(q)
+    for out in ((part(8), part(2 * n), part(3 * n)), (part(n), part(2 * n - 8), part(4 * n)), (part(n), part(2 * n), part(n - 8))):
+        with pytest.raises(vsa.VsaError):
+            plan.backward(do, part(0), k, v, o, lse, kinds=kinds, out=out)
+    grads = plan.backward(do, part(0), k, v, o, lse, kinds=kinds, out=(part(n), part(2 * n), part(3 * n)))
+    for a, b in zip(grads, plan.backward(do, q, k, v, o, lse, kinds=kinds)):
+        assert torch.equal(a, b)
+    shape, err = _lib.make_shape(1, 2, 1, 1, 300, 64, 64), cuda_err()
+    idx, cnt = torch.zeros(1, 2, 5, 1, dtype=torch.int32, device="cuda"), torch.ones(1, 2, 5, dtype=torch.int32, device="cuda")
+    need = _lib.vsa_sparse_attn_bwd_workspace_size(shape)
+    for dq, ws in ((part(8), torch.empty(need, dtype=torch.uint8, device="cuda")), (part(n), part(0).view(torch.uint8).flatten())):
+        with pytest.raises(vsa.VsaError) as e:
+            _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(part(0), k, v, o, do, lse, dq, part(2 * n), part(3 * n)), None, kinds, idx, cnt, 1,
+                                     shape, 0.0, ws, need, err)
+        assert e.value.status == _lib.VSA_ERR_INVALID_ARG
