@@ -458,7 +458,7 @@ class RMSNorm:
                           new(*shape, dtype=torch.uint8) if self.quantize else None,
                           new(*shape[:2], -(-self.N // self.quantize), dtype=torch.int32) if self.quantize else None,
                           new(*shape[:3], dtype=torch.float32))
-            vsa_rms_norm(x, residual, _DTYPE[self.dtype], weight, wt, self._shape(x, residual), out.sum, out.y,
+            _lib._rms_norm(x, residual, _DTYPE[self.dtype], weight, wt, self._shape(x, residual), out.sum, out.y,
                          out.codes, out.exps, out.rstd)
         return out
 
@@ -485,7 +485,7 @@ class RMSNorm:
             dx = (torch.empty_strided(shape, s.stride(), dtype=s.dtype, device=self.device) if _whole_rows(s)
                   else torch.empty(shape, dtype=s.dtype, device=self.device))
             dw = torch.empty(self.d, dtype=torch.float32, device=self.device) if weight is not None else None
-            vsa_rms_norm_bwd(dy, d_sum, s, _DTYPE[self.dtype], weight, wt, rstd, self._shape(s, dx), dx, dw, self.ws,
+            _lib._rms_norm_bwd(dy, d_sum, s, _DTYPE[self.dtype], weight, wt, rstd, self._shape(s, dx), dx, dw, self.ws,
                              self.ws.numel())
         return dx, dw
 

@@ -53,6 +53,7 @@ class HostBatch(ctypes.Structure):
 
 
 class QKVO(ctypes.Structure):
+    held = None  # the tensors behind the addresses (qkvo)
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("o", ctypes.c_void_p),
                 ("lse", ctypes.c_void_p)]
 
@@ -298,7 +299,9 @@ def vsa_build_mask(kinds, q_cube, k_cube, shape: Shape, params: Params, bits, kv
 
 
 def qkvo(q, k, v, o, lse=None) -> QKVO:
-    return QKVO(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse))
+    out = QKVO(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse))
+    out.held = (q, k, v, o, lse)
+    return out
 
 
 def vsa_block_order(kinds, kv_idx, kv_cnt, max_kv, shape: Shape, order, stream=None):
@@ -358,10 +361,53 @@ def vsa_attention(io: QKVO, dtype: int, shape: Shape, params: Params, select: in
 def qkvo_grad(q, k, v, o, d_o, lse, dq, dk, dv, d_lse=None, o_lo=None) -> QKVOGrad:
     """One set of the gradient's tensors (or addresses).  lse and d_lse may have their rows anywhere, as in rows cut
     out of longer ones: the calls copy them where they are not whole rows on 16 bytes."""
-    all_ = (q, k, v, o, d_o, lse, d_lse, dq, dk, dv, o_lo)
-    out = QKVOGrad(*(_ptr(t) for t in all_))
-    out.held = {f[0]: t for f, t in zip(QKVOGrad._fields_, all_) if isinstance(t, torch.Tensor)}
+    out = QKVOGrad(*map(_ptr, (q, k, v, o, d_o, lse, d_lse, dq, dk, dv, o_lo)))
+    out.held = (lse, d_lse, (q, k, v, o, d_o, dq, dk, dv, o_lo))
     return out
+
+
+def _expect(t, dtypes, numel: int, what: str):
+    """A tensor that the library is given as an address is what it will be read as; addresses pass."""
+    if isinstance(t, torch.Tensor) and (t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous {' or '.join(map(str, dtypes))} tensor of {numel} elements expected, "
+                         f"not {t.dtype} of shape {tuple(t.shape)} and strides {t.stride()}")
+
+
+def _expect_scratch(ws, ws_bytes: int, err):
+    if isinstance(ws, torch.Tensor) and (not ws.is_contiguous() or ws.numel() * ws.element_size() < ws_bytes):
+        raise ValueError(f"the workspace does not hold {ws_bytes} contiguous bytes")
+    if isinstance(err, torch.Tensor) and (err.dtype != torch.int32 or err.numel() == 0):
+        raise ValueError("the error word is an int32 tensor")
+
+
+_TYPES = {VSA_F32: (torch.float32,), VSA_BF16: (torch.bfloat16,)}
+_I32, _U8 = (torch.int32,), (torch.uint8,)
+
+
+def _geometry(shape: Shape):
+    """Heads, natural rows and permuted rows of a head; None for a shape that the library refuses."""
+    heads, n = shape.B * shape.H, shape.F * shape.Hl * shape.Wl
+    if min(shape.B, shape.H, shape.F, shape.Hl, shape.Wl, shape.block) <= 0:
+        return None
+    c = (shape.cube_f, shape.cube_h, shape.cube_w)
+    if c == (0, 0, 0):
+        return heads, n, n
+    if min(c) <= 0:
+        return None
+    return heads, n, -(-shape.F // c[0]) * -(-shape.Hl // c[1]) * -(-shape.Wl // c[2]) * c[0] * c[1] * c[2]
+
+
+def _expect_set(s: QKVOGrad, rows: int, d: int, dtypes, what: str):
+    if s.held is None:
+        return
+    lse, d_lse, big = s.held
+    numel, dtype = rows * d, dtypes[0]
+    for t in big:
+        if t is not None and isinstance(t, torch.Tensor) and (t.dtype is not dtype or t.numel() != numel or not t.is_contiguous()):
+            _expect(t, dtypes, numel, f"q, k, v, o, d_o, dq, dk, dv and o_lo of the {what} set")
+    for t in (lse, d_lse):
+        if isinstance(t, torch.Tensor) and (t.dtype != torch.float32 or t.numel() != rows):
+            raise ValueError(f"lse and d_lse of the {what} set: float32 tensors of {rows} elements expected")
 
 
 def _on_16_bytes(t: torch.Tensor) -> torch.Tensor:
@@ -374,19 +420,16 @@ def _on_16_bytes(t: torch.Tensor) -> torch.Tensor:
 def _whole_rows(s, stream):
     """The set with lse and d_lse in whole rows on 16 bytes, copied on `stream` where they are not; the second value
     holds the copies."""
-    copies = {}
-    if s is not None and s.held:
-        for name in ("lse", "d_lse"):
-            t = s.held.get(name)
-            if t is not None and not (t.is_contiguous() and t.data_ptr() % 16 == 0):
+    copies = []
+    if s is not None and s.held is not None:
+        for name, t in (("lse", s.held[0]), ("d_lse", s.held[1])):
+            if isinstance(t, torch.Tensor) and not (t.is_contiguous() and t.data_ptr() % 16 == 0):
+                if not copies:
+                    s = QKVOGrad.from_buffer_copy(s)
                 with _on(stream, t.device):
-                    copies[name] = _on_16_bytes(t)
-    if not copies:
-        return s, copies
-    out = QKVOGrad.from_buffer_copy(s)
-    for name, t in copies.items():
-        setattr(out, name, t.data_ptr())
-    return out, copies
+                    copies.append(_on_16_bytes(t))
+                setattr(s, name, copies[-1].data_ptr())
+    return s, copies
 
 
 def vsa_attention_train_workspace_size(shape: Shape, params: Params, dtype: int, select: int) -> int:
@@ -395,6 +438,14 @@ def vsa_attention_train_workspace_size(shape: Shape, params: Params, dtype: int,
 
 def vsa_attention_train(io: QKVO, o_lo, dtype: int, shape: Shape, params: Params, select: int, kinds, mse, ws, ws_bytes,
                         err, stream=None):
+    geometry, dtypes = _geometry(shape), _TYPES.get(dtype)
+    if geometry is not None and dtypes is not None:
+        rows = geometry[0] * geometry[1]
+        for t in (*(io.held or ())[:4], o_lo):
+            _expect(t, dtypes, rows * shape.d, "q, k, v, o and o_lo")
+        _expect(io.held and io.held[4], _TYPES[VSA_F32], rows, "lse")
+        _expect(kinds, _U8, geometry[0], "kinds")
+        _expect_scratch(ws, ws_bytes, err)
     _check(lib.vsa_attention_train(ctypes.byref(io), _ptr(o_lo), dtype, ctypes.byref(shape), ctypes.byref(params), select,
                                    _ptr(kinds), _ptr(mse), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)),
            "vsa_attention_train")
@@ -406,6 +457,17 @@ def vsa_sparse_attn_bwd_workspace_size(shape: Shape) -> int:
 
 def vsa_sparse_attn_bwd(natural: QKVOGrad, permuted, kinds, kv_idx, kv_cnt, max_kv, shape: Shape, scale, ws, ws_bytes,
                         err, stream=None):
+    geometry = _geometry(shape)
+    if geometry is not None:
+        heads, n, r = geometry
+        _expect_set(natural, heads * (n if permuted is not None else r), shape.d, _TYPES[VSA_BF16], "natural")
+        if permuted is not None:
+            _expect_set(permuted, heads * r, shape.d, _TYPES[VSA_BF16], "permuted")
+        lists = heads * -(-r // shape.block)
+        _expect(kinds, _U8, heads, "kinds")
+        _expect(kv_idx, _I32, lists * int(max_kv), "kv_idx")
+        _expect(kv_cnt, _I32, lists, "kv_cnt")
+        _expect_scratch(ws, ws_bytes, err)
     natural, copies = _whole_rows(natural, stream)
     permuted, more = _whole_rows(permuted, stream)
     _check(lib.vsa_sparse_attn_bwd(ctypes.byref(natural), ctypes.byref(permuted) if permuted is not None else None,
@@ -419,6 +481,11 @@ def vsa_attention_bwd_workspace_size(shape: Shape, params: Params, dtype: int) -
 
 
 def vsa_attention_bwd(io: QKVOGrad, dtype: int, shape: Shape, params: Params, kinds, ws, ws_bytes, err, stream=None):
+    geometry, dtypes = _geometry(shape), _TYPES.get(dtype)
+    if geometry is not None and dtypes is not None:
+        _expect_set(io, geometry[0] * geometry[1], shape.d, dtypes, "call's")
+        _expect(kinds, _U8, geometry[0], "kinds")
+        _expect_scratch(ws, ws_bytes, err)
     io, copies = _whole_rows(io, stream)
     _check(lib.vsa_attention_bwd(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
                                  _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention_bwd")
@@ -433,8 +500,41 @@ def make_norm_shape(B, H, N, d, x_stride=(0, 0, 0), res_stride=(0, 0, 0), block=
     return NormShape(int(B), int(H), int(N), int(d), i3(*x_stride), i3(*res_stride), int(block), float(eps))
 
 
+def _expect_rows(t, dtypes, sizes, strides, what: str):
+    """Rows of a norm: contiguous where the strides are 0, else all of them inside the tensor's memory."""
+    if not isinstance(t, torch.Tensor):
+        return
+    if not any(strides):
+        _expect(t, dtypes, sizes[0] * sizes[1] * sizes[2] * sizes[3], what)
+        return
+    last = sum((n - 1) * st for n, st in zip(sizes, strides)) + sizes[3]
+    if t.dtype not in dtypes or (t.storage_offset() + last) * t.element_size() > t.untyped_storage().nbytes():
+        raise ValueError(f"{what}: {dtypes[0]} rows at strides {tuple(strides)} do not lie inside a {t.dtype} tensor of "
+                         f"shape {tuple(t.shape)}")
+
+
+def _norm_sizes(shape: NormShape):
+    sizes = (shape.B, shape.H, shape.N, shape.d)
+    return sizes if min(sizes) > 0 and shape.block > 0 else None
+
+
 def vsa_rms_norm(x, residual, dtype: int, weight, weight_dtype: int, shape: NormShape, sum=None, y=None, codes=None,
                  exps=None, rstd=None, stream=None):
+    sizes, dtypes = _norm_sizes(shape), _TYPES.get(dtype)
+    if sizes is not None and dtypes is not None:
+        rows = sizes[0] * sizes[1] * sizes[2]
+        _expect_rows(x, dtypes, sizes, shape.x_stride, "x")
+        _expect_rows(residual, dtypes, sizes, shape.res_stride, "the residual")
+        _expect(weight, _TYPES.get(weight_dtype, ()), shape.d, "the weight")
+        _expect(sum, dtypes, rows * shape.d, "sum")
+        _expect(y, dtypes, rows * shape.d, "y")
+        _expect(codes, (torch.uint8, torch.float8_e4m3fn), rows * shape.d, "codes")
+        _expect(exps, _I32, sizes[0] * sizes[1] * -(-shape.N // shape.block), "the exponents")
+        _expect(rstd, _TYPES[VSA_F32], rows, "rstd")
+    _rms_norm(x, residual, dtype, weight, weight_dtype, shape, sum, y, codes, exps, rstd, stream)
+
+
+def _rms_norm(x, residual, dtype, weight, weight_dtype, shape, sum, y, codes, exps, rstd, stream=None):
     _check(lib.vsa_rms_norm(_ptr(x), _ptr(residual), dtype, _ptr(weight), weight_dtype, ctypes.byref(shape), _ptr(sum),
                             _ptr(y), _ptr(codes), _ptr(exps), _ptr(rstd), _stream(stream)), "vsa_rms_norm")
 
@@ -445,6 +545,21 @@ def vsa_rms_norm_bwd_workspace_size(shape: NormShape, dtype: int) -> int:
 
 def vsa_rms_norm_bwd(dy, d_sum, s, dtype: int, weight, weight_dtype: int, rstd, shape: NormShape, dx, d_weight=None,
                      ws=None, ws_bytes=0, stream=None):
+    sizes, dtypes = _norm_sizes(shape), _TYPES.get(dtype)
+    if sizes is not None and dtypes is not None:
+        rows = sizes[0] * sizes[1] * sizes[2]
+        _expect(dy, dtypes, rows * shape.d, "dy")
+        _expect(d_sum, dtypes, rows * shape.d, "d_sum")
+        _expect_rows(s, dtypes, sizes, shape.x_stride, "s")
+        _expect_rows(dx, dtypes, sizes, shape.res_stride, "dx")
+        _expect(weight, _TYPES.get(weight_dtype, ()), shape.d, "the weight")
+        _expect(rstd, _TYPES[VSA_F32], rows, "rstd")
+        _expect(d_weight, _TYPES[VSA_F32], shape.d, "d_weight")
+        _expect_scratch(ws, ws_bytes, None)
+    _rms_norm_bwd(dy, d_sum, s, dtype, weight, weight_dtype, rstd, shape, dx, d_weight, ws, ws_bytes, stream)
+
+
+def _rms_norm_bwd(dy, d_sum, s, dtype, weight, weight_dtype, rstd, shape, dx, d_weight, ws, ws_bytes, stream=None):
     _check(lib.vsa_rms_norm_bwd(_ptr(dy), _ptr(d_sum), _ptr(s), dtype, _ptr(weight), weight_dtype, _ptr(rstd),
                                 ctypes.byref(shape), _ptr(dx), _ptr(d_weight), _ptr(ws), int(ws_bytes),
                                 _stream(stream)), "vsa_rms_norm_bwd")
