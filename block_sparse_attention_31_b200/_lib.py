@@ -182,10 +182,12 @@ def _there(stream, device):
     with torch.cuda.device(device):
         if stream is None:
             yield
-        else:
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                   else torch.cuda.ExternalStream(int(stream), device=device)):
-                yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            # torch takes the handle 0 of an external stream for none, and gives one of its own
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            yield
 
 
 def _on(stream, device):

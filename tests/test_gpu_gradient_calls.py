@@ -142,3 +142,25 @@ def test_outputs_over_inputs_are_refused():
             _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(part(0), k, v, o, do, lse, dq, part(2 * n), part(3 * n)), None, kinds, idx, cnt, 1,
                                      shape, 0.0, ws, need, err)
         assert e.value.status == _lib.VSA_ERR_INVALID_ARG
+
+
+def test_the_default_stream_by_its_handle():
+    """Stream 0 is the default stream, not one of torch's own."""
+    norm = vsa.RMSNorm(1, 2, 50, 64, with_grad=True)
+    x, w, dy = _rand(1, 2, 50, 64, seed=1), _rand(64, seed=2), _rand(1, 2, 50, 64, seed=3)
+    want = norm(x, w)
+    grads = norm.backward(dy, x, want.rstd, w)
+    late, late_dy = torch.zeros_like(x), torch.zeros_like(dy)
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(100_000_000)
+            late.copy_(x)
+            late_dy.copy_(dy)
+        got = norm(late, w, stream=0)
+        got_grads = norm.backward(late_dy, late, want.rstd, w, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got.y, want.y) and torch.equal(got.rstd, want.rstd)
+    for a, b in zip(got_grads, grads):
+        assert torch.equal(a, b)
