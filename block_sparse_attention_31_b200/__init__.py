@@ -139,7 +139,9 @@ class SparseAttention(_HostPipelined):
              qk_fp8.
 
     A plan's workspaces serve one call at a time: order calls on different streams, and graphs
-    that captured them, before they run, or give each its own plan.
+    that captured them, before they run, or give each its own plan.  A call runs, with all that it
+    reads (``kinds`` too) and allocates, on ``stream`` (a torch stream or a raw handle), by default the
+    device's current one.
     """
 
     def __init__(self, B: int, H: int, F: int, Hl: int, Wl: int, d: int, block: int = 128, *,
@@ -202,20 +204,21 @@ class SparseAttention(_HostPipelined):
                 raise ValueError("q, k, v must be contiguous tensors of the configured dtype and device")
             if tuple(t.shape) != (self.B, self.H, self.N, self.d):
                 raise ValueError(f"expected shape {(self.B, self.H, self.N, self.d)}, got {tuple(t.shape)}")
-        if out is None:
-            out = torch.empty_like(q)
-        if self.with_lse and lse is None:
-            lse = torch.empty(self.B, self.H, self.N, dtype=torch.float32, device=self.device)
-        if self.select == VSA_SELECT_GIVEN:
-            if kinds is None:
-                raise ValueError("select='given' needs kinds")
-            self.kinds.copy_(kinds.reshape(-1).to(torch.uint8))
-        if o_lo is not None:
-            vsa_attention_train(qkvo(q, k, v, out, lse), o_lo, _DTYPE[self.dtype], self.shape, self.params, self.select,
-                                self.kinds, self.mse, self.ws, self.ws_bytes, self.err, stream)
-        else:
-            vsa_attention(qkvo(q, k, v, out, lse), _DTYPE[self.dtype], self.shape, self.params, self.select, self.kinds,
-                          self.mse, self.ws, self.ws_bytes, self.err, stream)
+        if self.select == VSA_SELECT_GIVEN and kinds is None:
+            raise ValueError("select='given' needs kinds")
+        with _on(stream, self.device):
+            if out is None:
+                out = torch.empty_like(q)
+            if self.with_lse and lse is None:
+                lse = torch.empty(self.B, self.H, self.N, dtype=torch.float32, device=self.device)
+            if self.select == VSA_SELECT_GIVEN:
+                self.kinds.copy_(kinds.reshape(-1).to(torch.uint8))
+            if o_lo is not None:
+                vsa_attention_train(qkvo(q, k, v, out, lse), o_lo, _DTYPE[self.dtype], self.shape, self.params, self.select,
+                                    self.kinds, self.mse, self.ws, self.ws_bytes, self.err)
+            else:
+                vsa_attention(qkvo(q, k, v, out, lse), _DTYPE[self.dtype], self.shape, self.params, self.select, self.kinds,
+                              self.mse, self.ws, self.ws_bytes, self.err)
         return (out, lse) if self.with_lse else out
 
     def backward(self, d_o: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
@@ -346,12 +349,12 @@ class SemanticAttention(_HostPipelined):
                 raise ValueError("q, k, v must be contiguous bf16 tensors on the configured device")
             if tuple(t.shape) != (self.B, self.H, self.N, self.d):
                 raise ValueError(f"expected shape {(self.B, self.H, self.N, self.d)}, got {tuple(t.shape)}")
-        if out is None:
-            out = torch.empty_like(q)
-        if self.with_lse and lse is None:
-            lse = torch.empty(self.B, self.H, self.N, dtype=torch.float32, device=self.device)
-        vsa_semantic_attention(qkvo(q, k, v, out, lse), self.shape, self.params, self.ws, self.ws_bytes, self.err,
-                               stream)
+        with _on(stream, self.device):
+            if out is None:
+                out = torch.empty_like(q)
+            if self.with_lse and lse is None:
+                lse = torch.empty(self.B, self.H, self.N, dtype=torch.float32, device=self.device)
+            vsa_semantic_attention(qkvo(q, k, v, out, lse), self.shape, self.params, self.ws, self.ws_bytes, self.err)
         return (out, lse) if self.with_lse else out
 
     def device_error(self) -> int:

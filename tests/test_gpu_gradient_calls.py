@@ -164,3 +164,45 @@ def test_the_default_stream_by_its_handle():
     assert torch.equal(got.y, want.y) and torch.equal(got.rstd, want.rstd)
     for a, b in zip(got_grads, grads):
         assert torch.equal(a, b)
+
+
+def test_forward_on_another_stream_with_its_own_kinds():
+    """The kinds of a call on another stream are its own, however late the current stream is."""
+    plan, q, k, v, _ = _small()
+    first, other = (torch.tensor(x, dtype=torch.uint8, device="cuda") for x in ([S_, T_], [T_, S_]))
+    want = [t.clone() for t in plan(q, k, v, kinds=other)]
+    plan(q, k, v, kinds=first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(400_000_000)                # the current stream is busy for some 0.2 s
+    for stream in (side, side.cuda_stream):
+        got = plan(q, k, v, kinds=other, stream=stream)
+        side.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("which", ["sparse", "semantic"])
+def test_outputs_on_another_stream_are_that_streams(which):
+    """What a call on another stream allocates is not memory that the current stream still writes."""
+    if which == "sparse":
+        plan, q, k, v, _ = _small()
+        kinds = torch.tensor([S_, T_], dtype=torch.uint8, device="cuda")
+        call = lambda **kw: plan(q, k, v, kinds=kinds, **kw)[0]  # noqa: E731
+    else:
+        sem = vsa.SemanticAttention(1, 2, 5, 6, 10, 64, 64, cq=4, ck=4, iters=2)
+        q, k, v = (_rand(1, 2, 300, 64, seed=s) for s in range(3))
+        call = lambda **kw: sem(q, k, v, **kw)  # noqa: E731
+    want = call().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    late = [torch.empty_like(q) for _ in range(8)]
+    torch.cuda._sleep(200_000_000)
+    for x in late:
+        x.fill_(7.0)
+    del x, late                                   # free for the current stream, which still has to write them
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
