@@ -1,5 +1,7 @@
 """GPU checks of how the gradient and the norm are called: strided and unaligned arguments, streams, threads, unknown
 head kinds, heads of unlike layouts beside each other."""
+import threading
+
 import pytest
 import torch
 
@@ -206,3 +208,46 @@ def test_outputs_on_another_stream_are_that_streams(which):
     got = call(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def _at_once(jobs, times):
+    """Each job `times` times on a thread and a stream of its own; what they raised."""
+    start, raised = threading.Barrier(len(jobs)), []
+
+    def work(job):
+        start.wait()
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(times):
+                    job()
+        except Exception as e:  # noqa: BLE001
+            raised.append(f"{type(e).__name__}: {e}")
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return raised
+
+
+def _attention(nb, gradient):
+    N, d = nb * 64, 64
+    shape = _lib.make_shape(1, 1, 1, 1, N, d, 64)
+    idx = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, 1, nb, 1)
+    cnt, kinds, err = torch.ones(1, 1, nb, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.uint8, device="cuda"), cuda_err()
+    q, o, lse = _rand(1, 1, N, d), _rand(1, 1, N, d), torch.zeros(1, 1, N, device="cuda")
+    if not gradient:
+        return lambda: _lib.vsa_sparse_attn_fwd(_lib.qkvo(q, q, q, o, lse), None, kinds, idx, cnt, 1, shape, 0.0, err)
+    ws = torch.empty(_lib.vsa_sparse_attn_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    grads = [torch.empty_like(q) for _ in range(3)]
+    return lambda: _lib.vsa_sparse_attn_bwd(_lib.qkvo_grad(q, q, q, o, o, lse, *grads), None, kinds, idx, cnt, 1, shape, 0.0, ws,
+                                            ws.numel(), err)
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+def test_first_call_of_a_thread(gradient):
+    """A thread whose first work on the device is the library's launch."""
+    torch.cuda.synchronize()
+    assert _at_once([_attention(2, gradient)], 1) == []
