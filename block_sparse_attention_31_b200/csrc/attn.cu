@@ -710,8 +710,8 @@ static cudaError_t launch_attn_t(const AttnMaps& nat, const AttnMaps& perm, cons
   auto kern = sparse_attn_fwd_kernel<D, BN, QK8>;
   const int nwords = (a.g.nblk + 31) / 32;
   const int smem = C::smem_bytes(a.ucap, nwords);
-  if (smem > 232448) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   const long long grid = static_cast<long long>(a.BH) * ((a.g.nblk + 1) / 2);
   if (grid <= 0) return cudaSuccess;

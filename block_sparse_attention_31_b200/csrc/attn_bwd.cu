@@ -61,7 +61,6 @@ namespace {
 constexpr int kBwdThreads = 384;
 constexpr int kWarpX = 8, kWarpMma = 9, kWarpY = 10, kWarpT = 11;
 constexpr int kBM = 128;
-constexpr int kMaxSmem = 232448;
 constexpr int kRegsSoftmax = 208, kRegsCtl = 88;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl == 384 * 168, "register split must equal the launch total");
 
@@ -729,7 +728,7 @@ cudaError_t launch_bwd_t(const BwdMaps& nat, const BwdMaps& perm, BwdArgs a, cud
   a.nx = C::stages(nwords);
   const int smem = C::smem_bytes(a.nx, nwords);
   if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   // may start while the last prep CTAs still run (programmatic dependent launch): everything up to
   // pdl_wait() in the kernel needs only what was there before prep

@@ -87,6 +87,17 @@ struct AttnArgs {
 cudaError_t launch_sparse_attn(const AttnMaps& nat, const AttnMaps& perm, const AttnArgs& a, int d,
                                cudaStream_t stream);
 
+// Shared memory of a CTA on sm_100a.
+constexpr int kMaxSmem = 232448;
+
+// Lets launches of a kernel ask for up to `most` bytes of dynamic shared memory.  The limit is the kernel's, for every
+// thread of the process: `most` is what its largest launch takes, never the size of the launch at hand, which another
+// thread's launch of the same kernel might then exceed.
+template <typename K>
+cudaError_t allow_smem(K* kern, int most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Gradient of the attention (see attn_bwd.cu): tensor maps of one set, the row terms and row
 // bitsets, and the main kernel's arguments.
 struct BwdMaps {

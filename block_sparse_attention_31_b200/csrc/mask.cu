@@ -455,10 +455,9 @@ cudaError_t launch_block_order(const uint8_t* kinds, const Geom& g, int BH, cons
   int n2 = 1;
   while (n2 < g.nblk) n2 <<= 1;
   const size_t smem = sizeof(uint32_t) * n2;
-  if (smem > 232448) return cudaErrorInvalidValue;
+  if (smem > kMaxSmem) return cudaErrorInvalidValue;
   if (smem > 48 * 1024) {
-    cudaError_t e =
-        cudaFuncSetAttribute(block_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(block_order_kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   block_order_kernel<<<BH, kOrderThreads, smem, stream>>>(kinds, g, kv_idx, kv_cnt, max_kv, n2, order);
@@ -487,9 +486,9 @@ cudaError_t launch_cube_mask(const uint8_t* kinds, const void* q_cube, const voi
   if (e != cudaSuccess) return e;
   const int nwords = (g.nblk + 31) >> 5;
   const size_t smem = (sizeof(uint64_t) + sizeof(int)) * kTopkWarps * kTopkCap + sizeof(uint32_t) * kTopkWarps * nwords;
-  if (smem > 232448) return cudaErrorInvalidConfiguration;
+  if (smem > kMaxSmem) return cudaErrorInvalidConfiguration;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(cube_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = allow_smem(cube_topk_kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   cube_topk_kernel<<<dim3((C + kTopkWarps - 1) / kTopkWarps, BH), kTopkWarps * 32, smem, stream>>>(

@@ -687,7 +687,7 @@ cudaError_t launch_norm_t(NormArgs a, cudaStream_t stream) {
       if (a.res == nullptr && a.d == 2 * H::TPR * H::VEC) {
         auto kern = rms_norm_block_kernel<T, H::VEC, H::TPR, H::ROWS>;
         const int smem = 2 * H::ROWS * 2 * 16 * threads;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = allow_smem(kern, 2 * H::ROWS * 2 * 16 * (128 * H::TPR / H::ROWS));  // blocks of 128 rows
         if (e != cudaSuccess) return e;
         const long long most = 148 * (1024 / threads);  // 64 registers a thread
         kern<<<static_cast<unsigned>(grid < most ? grid : most), threads, smem, stream>>>(a);
@@ -717,20 +717,17 @@ cudaError_t launch_norm_bwd_t(NormBwdArgs a, float* dw, cudaStream_t stream) {
     const long long items = static_cast<long long>(a.n.chunks) * a.n.BH;
     const int most = bwd_ctas<H>(n), grid = static_cast<int>(items < most ? items : most);
     cudaError_t e;
-    auto launch = [&](auto kern, int smem) {
-      const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (r == cudaSuccess) kern<<<grid, threads, smem, stream>>>(a);
-      return r;
-    };
     // two stages take at most 192 KB for 512 threads, as many as an SM holds; fp32 rows of over 8192 take more
     constexpr bool kVec = H::VEC > 1, kLong = sizeof(T) == 4 && H::TPR == 0 && H::NV == 4;
+    constexpr int kArray = 2 * H::ROWS * H::NV * 16;  // bytes a thread for each of s, dy and d_sum
     if (kVec && threads <= 512) {
-      const int smem = 2 * (a.d_sum != nullptr ? 3 : 2) * H::ROWS * H::NV * 16 * threads;
-      e = launch(rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec>, smem);
+      auto kern = rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec>;
+      e = allow_smem(kern, 3 * kArray * (H::TPR != 0 ? 256 : 512));
+      if (e != cudaSuccess) return e;
+      kern<<<grid, threads, (a.d_sum != nullptr ? 3 : 2) * kArray * threads, stream>>>(a);
     } else {
-      e = launch(rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec && !kLong>, 0);
+      rms_norm_bwd_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, kVec && !kLong><<<grid, threads, 0, stream>>>(a);
     }
-    if (e != cudaSuccess) return e;
     e = cudaGetLastError();
     if (e != cudaSuccess || dw == nullptr) return e;
     rms_norm_dw_kernel<<<(a.n.d + 31) / 32, 1024, 0, stream>>>(a.partial, grid, a.n.d, dw);

@@ -1008,8 +1008,7 @@ cudaError_t kmeans_d(const __nv_bfloat16* x, int BH, int N, int C, int iters, fl
   if (e != cudaSuccess) return e;
   const size_t ssmem = sizeof(int) * kSortWarps * static_cast<size_t>(C);
   if (ssmem > 48 * 1024) {
-    e = cudaFuncSetAttribute(kmeans_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(ssmem));
+    e = allow_smem(kmeans_scatter_kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   CUtensorMap tx, thi, tlo;

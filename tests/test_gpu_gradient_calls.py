@@ -251,3 +251,26 @@ def test_first_call_of_a_thread(gradient):
     """A thread whose first work on the device is the library's launch."""
     torch.cuda.synchronize()
     assert _at_once([_attention(2, gradient)], 1) == []
+
+
+def _norm_gradient(d, with_sum):
+    norm = vsa.RMSNorm(1, 1, 4, d, with_grad=True)
+    x, dy, ds = (_rand(1, 1, 4, d, seed=s) for s in range(3))
+    w = _rand(d, seed=4)
+    rstd = norm(x, w).rstd
+    return lambda: norm.backward(dy, x, rstd, w, d_sum=ds if with_sum else None)
+
+
+def _norm_codes(block):
+    norm, x = vsa.RMSNorm(1, 1, 200, 128, quantize=block), _rand(1, 1, 200, 128)
+    return lambda: norm(x)
+
+
+@pytest.mark.parametrize("what", ["norm gradient", "norm codes", "attention gradient", "attention"])
+def test_threads_launch_one_kernel_in_unlike_sizes(what):
+    """Launches of one kernel with more and with less shared memory, from two threads at a time, all start."""
+    make = {"norm gradient": lambda: [_norm_gradient(1536, False), _norm_gradient(1536, True)],
+            "norm codes": lambda: [_norm_codes(64), _norm_codes(128)],
+            "attention gradient": lambda: [_attention(2, True), _attention(4000, True)],
+            "attention": lambda: [_attention(2, False), _attention(4000, False)]}[what]
+    assert _at_once(make() + make(), 3000) == []
