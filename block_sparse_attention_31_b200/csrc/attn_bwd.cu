@@ -204,7 +204,7 @@ __device__ __forceinline__ void bwd_cta(const BwdMaps* mn, const BwdMaps* mp, co
   const int nwords = (g.nblk + 31) >> 5;
   const int kind = a.kinds[bh];
 
-  if (kind > kCube || (kind == kCube && g.ncubes == 0)) {
+  if (!known_kind(g, kind)) {
     // unknown layout: this block's rows of the natural-order gradients become zeros
     pdl_wait();
     if (tid == 0 && blk == 0) atomicOr(a.err, kDevErrKind);
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
     if (row >= static_cast<long long>(a.BH) * g.nblk) return;
     const int bh = static_cast<int>(row / g.nblk), i = static_cast<int>(row - static_cast<long long>(bh) * g.nblk);
     const int kind = a.kinds[bh];
-    const int nb = kind > kCube ? 0 : (layout_rows(g, kind) + g.block - 1) / g.block;
+    const int nb = known_kind(g, kind) ? (layout_rows(g, kind) + g.block - 1) / g.block : 0;
     const int32_t* list = a.kv_idx + row * a.max_kv;
     uint32_t* out = a.rbits + row * nwords;
     const int cnt = i < nb ? a.kv_cnt[row] : 0;
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prep_kernel(const BwdPrep a)
     const long long at = min(first + r * groups, all - 1);
     const int bh = static_cast<int>(at / slots), slot = static_cast<int>(at - static_cast<long long>(bh) * slots);
     const int kind = a.kinds[bh];
-    const int token = kind <= kCube && !(kind == kCube && g.ncubes == 0) ? token_of_slot(g, kind, slot) : -1;
+    const int token = known_kind(g, kind) ? token_of_slot(g, kind, slot) : -1;
     has[r] = token >= 0;
     // whole call: O, dO and LSE in natural order; lists: each head's own layout and set.  A slot without a
     // token loads row 0 of its head.

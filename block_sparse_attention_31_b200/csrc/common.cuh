@@ -30,6 +30,11 @@ __host__ __device__ __forceinline__ int layout_rows(const Geom& g, int kind) {
   return kind == kCube ? g.ncubes * g.vol : g.N;
 }
 
+// Whether `kind` is a layout of this grid: a known kind, and not cubes where none are set.
+__host__ __device__ __forceinline__ bool known_kind(const Geom& g, int kind) {
+  return kind < kCube || (kind == kCube && g.ncubes > 0);
+}
+
 // Slot of natural token t under `kind`.
 __host__ __device__ __forceinline__ int slot_of_token(const Geom& g, int kind, int t) {
   if (kind == kSpatial) return t;

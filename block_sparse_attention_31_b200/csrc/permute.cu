@@ -59,12 +59,12 @@ __global__ void __launch_bounds__(kPermThreads) permute_kernel(const void* __res
                                                                int* err) {
   const int bh = blockIdx.y;
   const int kind = kinds[bh];
-  if (kind > kCube) {
+  if (!known_kind(g, kind)) {
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(err, kDevErrKind);
     return;
   }
   if (!kSrcF32 && kind == kSpatial) return;
-  if (kind == kCube && g.ncubes > 0) return;  // cube_permute_kernel
+  if (kind == kCube) return;  // cube_permute_kernel
   const int vpr = d / 8;  // 16-byte vectors per row
   const int rows_per_pass = kPermThreads / vpr;
   const int v = threadIdx.x % vpr;
@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_kernel(const void* __res
   }
 }
 
-// dst[bh, t] = src[bh, slot_of_token(t)] (converted to the destination type); same for LSE.
+// dst[bh, t] = src[bh, slot_of_token(t)] (converted to the destination type); same for LSE.  A head of unknown layout
+// gets zeros and an LSE of -inf: whoever reads dst reads what nothing has computed otherwise.
 template <bool kDstF32>
 __global__ void __launch_bounds__(kPermThreads) unpermute_kernel(const __nv_bfloat16* __restrict__ src,
                                                                  const float* __restrict__ src_lse,
@@ -97,12 +98,10 @@ __global__ void __launch_bounds__(kPermThreads) unpermute_kernel(const __nv_bflo
                                                                  int* err) {
   const int bh = blockIdx.y;
   const int kind = kinds[bh];
-  if (kind > kCube) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(err, kDevErrKind);
-    return;
-  }
+  const bool known = known_kind(g, kind);
+  if (!known && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(err, kDevErrKind);
   if (!kDstF32 && kind == kSpatial) return;
-  if (kind == kCube && g.ncubes > 0) return;  // cube_unpermute_kernel
+  if (known && kind == kCube) return;  // cube_unpermute_kernel
   const int vpr = d / 8;
   const int rows_per_pass = kPermThreads / vpr;
   const int v = threadIdx.x % vpr;
@@ -116,8 +115,8 @@ __global__ void __launch_bounds__(kPermThreads) unpermute_kernel(const __nv_bflo
 #pragma unroll
     for (int u = 0; u < kPermUnroll; ++u) {
       tok[u] = base + u * rows_per_pass + r0;
-      slot[u] = tok[u] < g.N ? slot_of_token(g, kind, tok[u]) : 0;
-      val[u] = tok[u] < g.N ? __ldg(reinterpret_cast<const uint4*>(src + src_head + static_cast<size_t>(slot[u]) * d +
+      slot[u] = known && tok[u] < g.N ? slot_of_token(g, kind, tok[u]) : 0;
+      val[u] = known && tok[u] < g.N ? __ldg(reinterpret_cast<const uint4*>(src + src_head + static_cast<size_t>(slot[u]) * d +
                                                                    v * 8))
                             : make_uint4(0, 0, 0, 0);
     }
@@ -126,7 +125,8 @@ __global__ void __launch_bounds__(kPermThreads) unpermute_kernel(const __nv_bflo
       if (tok[u] >= g.N) continue;
       store8_from_bf16(dst, dst_head + static_cast<size_t>(tok[u]) * d + v * 8, val[u], kDstF32);
       if (src_lse != nullptr && dst_lse != nullptr && v == 0)
-        dst_lse[static_cast<size_t>(bh) * g.N + tok[u]] = src_lse[static_cast<size_t>(bh) * g.R + slot[u]];
+        dst_lse[static_cast<size_t>(bh) * g.N + tok[u]] =
+            known ? src_lse[static_cast<size_t>(bh) * g.R + slot[u]] : -INFINITY;
     }
   }
 }

@@ -187,7 +187,8 @@ VSA_API vsa_status vsa_permute(const void *src, vsa_dtype src_dtype, void *dst, 
  *   src      [B, H, R, d] bf16 in each head's layout;  src_lse [B, H, R] fp32 or NULL
  *   dst      [B, H, N, d] in dst_dtype, natural order;  dst_lse [B, H, N] or NULL
  * Spatial heads are left untouched when dst is bf16 (their output is written in place by
- * vsa_sparse_attn_fwd); when dst is fp32 every head is converted.
+ * vsa_sparse_attn_fwd); when dst is fp32 every head is converted.  A head of unknown kind (cubes
+ * without cube dims among them) sets VSA_DEVERR_KIND and gets zeros and a dst_lse of -inf.
  */
 VSA_API vsa_status vsa_unpermute(const void *src, const float *src_lse, void *dst, vsa_dtype dst_dtype, float *dst_lse,
                          const uint8_t *d_kind, const vsa_shape *shape, int *d_err, cudaStream_t stream);

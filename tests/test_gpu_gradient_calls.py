@@ -274,3 +274,28 @@ def test_threads_launch_one_kernel_in_unlike_sizes(what):
             "attention gradient": lambda: [_attention(2, True), _attention(4000, True)],
             "attention": lambda: [_attention(2, False), _attention(4000, False)]}[what]
     assert _at_once(make() + make(), 3000) == []
+
+
+@pytest.mark.parametrize("byte", [9, 2])
+@pytest.mark.parametrize("dtype,layout", [(BF, False), (BF, True), (F32, False)])
+def test_call_with_unknown_kinds(dtype, layout, byte):
+    """A head of unknown kind (a cube head without cubes among them): the error bit, a zero output that sees nothing and
+    zero gradients, and the other head as without it."""
+    plan, q, k, v, do = _small(dtype=dtype, layout_in_kernel=layout)
+    good, bad = (torch.tensor(x, dtype=torch.uint8, device="cuda") for x in ([T_, S_], [T_, byte]))
+    o, lse = plan(q, k, v, kinds=good)
+    want = plan.backward(do, q, k, v, o, lse, kinds=good)
+    assert plan.device_error() == 0
+    plan.ws.fill_(0x41)                            # rows of earlier calls are not zeros
+    plan.ws_bwd.fill_(0x41)
+    o2, lse2, o_lo = torch.full_like(o, 5.0), torch.full_like(lse, 5.0), torch.full_like(o, 5.0)
+    for lo in (None, o_lo):
+        plan(q, k, v, out=o2.fill_(5.0), lse=lse2.fill_(5.0), kinds=bad, o_lo=lo)
+        assert plan.device_error() & _lib.VSA_DEVERR_KIND
+        plan.clear_error()
+        assert torch.equal(o2[:, 0], o[:, 0]) and torch.equal(lse2[:, 0], lse[:, 0])
+        assert (o2[:, 1] == 0).all() and (lse2[:, 1] == -torch.inf).all() and (lo is None or (lo[:, 1] == 0).all())
+    grads = plan.backward(do, q, k, v, o, lse, kinds=bad, out=[torch.full_like(q, 9.0) for _ in range(3)])
+    assert plan.device_error() & _lib.VSA_DEVERR_KIND
+    for a, b in zip(grads, want):
+        assert (a[:, 1] == 0).all() and torch.equal(a[:, 0], b[:, 0])
