@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import _on
+from ._lib import _on, _on_16_bytes
 from ._lib import (VSA_BF16, VSA_CUBE, VSA_F32, VSA_SELECT_CUBE, VSA_SELECT_GIVEN, VSA_SELECT_PROFILE, VSA_SPATIAL,
                    VSA_TEMPORAL, Params, QKVO, Shape, VsaError, make_params, make_shape, qkvo, vsa_attention,
                    vsa_attention_workspace_layout, vsa_attention_workspace_size, vsa_block_order,
@@ -239,6 +239,7 @@ class SparseAttention(_HostPipelined):
             for t in (d_o, q, k, v, o, *out) if o_lo is None else (d_o, q, k, v, o, *out, o_lo):
                 if t.dtype != self.dtype or t.device != self.device or not t.is_contiguous() or tuple(t.shape) != shape:
                     raise ValueError(f"contiguous {self.dtype} tensors of shape {shape} on {self.device} expected")
+            d_o = _on_16_bytes(d_o)  # autograd may hand over a slice
             for t in (lse, d_lse):
                 if t is not None and (t.dtype != torch.float32 or t.device != self.device or tuple(t.shape) != shape[:3]):
                     raise ValueError(f"lse and d_lse are float32 tensors of shape {shape[:3]} on {self.device}")
@@ -404,7 +405,8 @@ class RMSNorm:
               workspace serves one call at a time.
 
     x and the residual are any views whose last dimension is dense, a [B, N, H, d] projection seen as
-    [B, H, N, d] among them; outputs are contiguous."""
+    [B, H, N, d] among them; outputs are contiguous.  A weight or gradient that does not start on 16 bytes
+    (one cut out of a larger buffer) is copied first."""
 
     def __init__(self, B: int, H: int, N: int, d: int, *, dtype: torch.dtype = torch.bfloat16, eps: float = 1e-6,
                  quantize: int = 0, keep_y: bool = False, with_grad: bool = False, device="cuda"):
@@ -437,22 +439,25 @@ class RMSNorm:
             raise ValueError(f"{what} is a {self.dtype} tensor of shape {shape} on {self.device}")
         if (self.d > 1 and t.stride(3) != 1) or (dense and not t.is_contiguous()):
             raise ValueError(f"{what} must be contiguous" if dense else f"the last dimension of {what} must be dense")
+        if dense:
+            return _on_16_bytes(t)
         # three zero strides are how the library is told of contiguous rows
         return t.contiguous() if not any(t.stride()[:3]) else t
 
-    def _weight(self, weight: Optional[torch.Tensor]) -> int:
+    def _weight(self, weight: Optional[torch.Tensor]):
+        """The weight on 16 bytes (it may be cut out of a flat buffer), and its type."""
         if weight is None:
-            return VSA_F32
+            return None, VSA_F32
         if weight.dtype not in _DTYPE or weight.device != self.device or tuple(weight.shape) != (self.d,) \
                 or not weight.is_contiguous():
             raise ValueError(f"weight is a contiguous float32 or bfloat16 tensor of shape {(self.d,)} on {self.device}")
-        return _DTYPE[weight.dtype]
+        return _on_16_bytes(weight), _DTYPE[weight.dtype]
 
     def __call__(self, x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
                  stream=None) -> NormOut:
-        wt = self._weight(weight)
         shape = (self.B, self.H, self.N, self.d)
         with _on(stream, self.device):
+            weight, wt = self._weight(weight)
             x = self._rows(x, "x")
             residual = None if residual is None else self._rows(residual, "the residual")
             new = lambda *sh, dtype: torch.empty(*sh, dtype=dtype, device=self.device)  # noqa: E731
@@ -476,14 +481,15 @@ class RMSNorm:
             if d_sum is not None:
                 raise ValueError("d_sum and dsum are one argument")
             d_sum = dsum
-        wt = self._weight(weight)
         with _on(stream, self.device):
+            weight, wt = self._weight(weight)
             dy = self._rows(dy, "dy", dense=True)
             d_sum = None if d_sum is None else self._rows(d_sum, "d_sum", dense=True)
             s = self._rows(s, "s")
             if rstd.dtype != torch.float32 or rstd.device != self.device or not rstd.is_contiguous() \
                     or tuple(rstd.shape) != (self.B, self.H, self.N):
                 raise ValueError("rstd is the float32 tensor the call returned")
+            rstd = _on_16_bytes(rstd)
             shape = (self.B, self.H, self.N, self.d)
             dx = (torch.empty_strided(shape, s.stride(), dtype=s.dtype, device=self.device) if _whole_rows(s)
                   else torch.empty(shape, dtype=s.dtype, device=self.device))

@@ -299,3 +299,43 @@ def test_call_with_unknown_kinds(dtype, layout, byte):
     assert plan.device_error() & _lib.VSA_DEVERR_KIND
     for a, b in zip(grads, want):
         assert (a[:, 1] == 0).all() and torch.equal(a[:, 0], b[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_arguments_off_16_bytes(dtype):
+    """A gradient that is a slice (as behind torch.cat), a weight out of one flat buffer: the bits of copies."""
+    B, H, N, d = 1, 1, 5, 7
+    norm = vsa.RMSNorm(B, H, N, d, dtype=dtype, with_grad=True)
+    x, res = (_rand(B, H, N, d, seed=s, dtype=dtype).requires_grad_() for s in (1, 2))
+    flat, go = _rand(d + 1, seed=3, dtype=dtype).requires_grad_(), _rand(5 * B, H, N, d, seed=4, dtype=dtype)
+    w = flat[1:]
+    assert w.data_ptr() % 16
+    y, s = norm.normalise(x, w, res)
+    z = norm.normalise(x, w)
+    got = torch.autograd.grad(torch.cat([z, y, s, y, y]), (x, flat, res), go)
+    w2 = w.detach().clone().requires_grad_()
+    y, s = norm.normalise(x, w2, res)
+    z = norm.normalise(x, w2)
+    loss = [(z, go[:1].clone()), (y, go[1:2] + go[3:4] + go[4:5]), (s, go[2:3].clone())]
+    want = torch.autograd.grad([a for a, _ in loss], (x, w2, res), [b for _, b in loss])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1][1:], want[1]) and torch.equal(got[2], want[2])
+    # the calls themselves
+    odd = torch.cat([go.flatten()[:1], go.flatten()])[1:].view(go.shape)
+    r = norm(x.detach(), w.detach(), residual=res.detach())
+    rstd = torch.cat([r.rstd.flatten()[:1], r.rstd.flatten()])[1:].view(r.rstd.shape)
+    dx, dw = norm.backward(odd[1:2], r.sum, rstd, w.detach(), d_sum=odd[2:3])
+    want = norm.backward(go[1:2].clone(), r.sum, r.rstd, w2.detach(), d_sum=go[2:3].clone())
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+def test_attention_gradient_off_16_bytes():
+    """The gradient of an output that went into one flat tensor behind a single element."""
+    plan, q, k, v, do = _small()
+    kinds = torch.tensor([S_, T_], dtype=torch.uint8, device="cuda")
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    one = torch.zeros(1, dtype=BF, device="cuda", requires_grad=True)
+    o = plan.attend(*leaves, kinds=kinds)
+    got = torch.autograd.grad(torch.cat([one, o.flatten()]), leaves, torch.cat([one.detach(), do.flatten()]))
+    want = torch.autograd.grad(plan.attend(*leaves, kinds=kinds), leaves, do)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
