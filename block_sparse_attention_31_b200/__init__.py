@@ -259,12 +259,13 @@ class SparseAttention(_HostPipelined):
     def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kinds: Optional[torch.Tensor] = None):
         """The call as a differentiable function: o whose ``backward`` fills the gradients of q, k and v
         (first derivatives; the masks count as constants).  Keeps q, k, v, o, o_lo, the log-sum-exp and
-        the kinds for the gradient.  Where autograd records it is refused under graph capture: capture
-        the call itself and ``backward`` instead."""
+        the kinds for the gradient, and nothing where autograd does not record.  Where it does, it is
+        refused under graph capture: capture the call itself and ``backward`` instead."""
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
-        if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
-            _no_capture("attend")
+        if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+            return self(q, k, v, kinds=kinds)[0]
+        _no_capture("attend")
         return _Attend.apply(self, q, k, v, kinds)
 
     def device_error(self) -> int:

@@ -339,3 +339,21 @@ def test_attention_gradient_off_16_bytes():
     want = torch.autograd.grad(plan.attend(*leaves, kinds=kinds), leaves, do)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_attend_keeps_nothing_where_no_gradient_is_recorded(monkeypatch):
+    plan, q, k, v, _ = _small()
+    kinds = torch.tensor([S_, T_], dtype=torch.uint8, device="cuda")
+    want = plan(q, k, v, kinds=kinds)[0]
+    leaf = q.clone().requires_grad_()
+
+    def refuse(*a, **kw):
+        raise AssertionError("the rounding errors were asked for")
+
+    monkeypatch.setattr(vsa, "vsa_attention_train", refuse)
+    assert torch.equal(plan.attend(q, k, v, kinds=kinds), want)
+    with torch.no_grad():
+        o = plan.attend(leaf, k, v, kinds=kinds)
+    assert torch.equal(o, want) and not o.requires_grad
+    with pytest.raises(AssertionError):
+        plan.attend(leaf, k, v, kinds=kinds)
