@@ -683,8 +683,10 @@ cudaError_t launch_norm_t(NormArgs a, cudaStream_t stream) {
       rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, false><<<gr, threads, 0, stream>>>(a);
       return cudaGetLastError();
     }
-    if constexpr (H::TPR != 0 && H::TPR <= 16 && H::VEC > 1 && H::NV == 2) {
-      if (a.res == nullptr && a.d == 2 * H::TPR * H::VEC) {
+    // blocks are of rows of 64 or 128, which these hold (64 elements read one by one leave half of their 128 empty)
+    constexpr int kHeld = H::NV * H::TPR * H::VEC;
+    if constexpr (H::VEC > 1 && (kHeld == 64 || kHeld == 128)) {
+      if (a.res == nullptr && a.d == kHeld) {
         auto kern = rms_norm_block_kernel<T, H::VEC, H::TPR, H::ROWS>;
         const int smem = 2 * H::ROWS * 2 * 16 * threads;
         const cudaError_t e = allow_smem(kern, 2 * H::ROWS * 2 * 16 * (128 * H::TPR / H::ROWS));  // blocks of 128 rows
@@ -694,7 +696,7 @@ cudaError_t launch_norm_t(NormArgs a, cudaStream_t stream) {
         return cudaGetLastError();
       }
     }
-    if constexpr (H::TPR != 0 && (H::NV <= 2 || H::VEC == 1)) {  // rows of 64 or 128
+    if constexpr (kHeld == 64 || kHeld == 128) {
       rms_norm_kernel<T, H::VEC, H::NV, H::TPR, H::ROWS, true><<<gr, threads, 0, stream>>>(a);
       return cudaGetLastError();
     }
