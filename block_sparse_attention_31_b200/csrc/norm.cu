@@ -122,6 +122,18 @@ __device__ __forceinline__ void v_fma(float* f, const float* a, const float* b) 
     for (int i = 0; i < N; ++i) f[i] = fmaf(a[i], b[i], f[i]);
   }
 }
+// f = a * c + f
+template <int N>
+__device__ __forceinline__ void v_fma(float* f, const float* a, float c) {
+  if constexpr (N % 2 == 0) {
+    const uint64_t c2 = f2_make(c, c);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) f2_split(f2_fma(f2_make(a[i], a[i + 1]), c2, f2_make(f[i], f[i + 1])), f[i], f[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fmaf(a[i], c, f[i]);
+  }
+}
 template <int N>
 __device__ __forceinline__ float v_dot(const float* a, const float* b) {
   if constexpr (N % 2 == 0) {
@@ -547,8 +559,8 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const int n = n0 + r * groups;
-      // dx = rstd * (dy * w) - (rstd^2 * mean) * s
-      const float c = -rstd[r] * rstd[r] * dot[r] * inv_d;
+      // dx = rstd * (dy * w - (rstd * mean) * s): rstd^2 may be beyond the floats where dx is not
+      const float c = -rstd[r] * (dot[r] * inv_d);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int col = (j * tpr + t) * VEC;
@@ -563,9 +575,8 @@ __global__ void __launch_bounds__(TPR != 0 ? 256 : sizeof(T) == 4 && VEC == 4 &&
           for (int i = 0; i < VEC; ++i) out[i] = 0.f;
         }
         v_scale<VEC>(fs, c);
-        v_add<VEC>(out, fs);
-        v_scale<VEC>(fy, rstd[r]);
-        v_fma<VEC>(out, fy, kHoldW ? w + j * VEC : wt);
+        v_fma<VEC>(fs, fy, kHoldW ? w + j * VEC : wt);
+        v_fma<VEC>(out, fs, rstd[r]);
         if (n < N && col < d) Chunk<T, VEC>::store(dx + static_cast<size_t>(n) * a.n.res_stride[2] + col, out);
       }
     }

@@ -357,3 +357,21 @@ def test_attend_keeps_nothing_where_no_gradient_is_recorded(monkeypatch):
     assert torch.equal(o, want) and not o.requires_grad
     with pytest.raises(AssertionError):
         plan.attend(leaf, k, v, kinds=kinds)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [128, 129, 1536, 16384])
+def test_norm_gradient_of_tiny_rows(d, dtype):
+    """Rows of 1e-18 without an eps: 1 / rms squared times the sums of a row is beyond the floats, the gradient is not."""
+    norm = vsa.RMSNorm(1, 1, 4, d, dtype=dtype, eps=0.0, with_grad=True)
+    x, w = (_rand(1, 1, 4, d, seed=1, dtype=F32) * 1e-18).to(dtype), _rand(d, seed=2, dtype=F32)
+    dy, ds = (100 * _rand(1, 1, 4, d, seed=3, dtype=F32)).to(dtype), _rand(1, 1, 4, d, seed=4, dtype=dtype)
+    dy[0, 0, 1] = 100 * (x[0, 0, 1].float() * 1e18).to(dtype)            # all of it along the row: it nearly cancels
+    rstd = norm(x, w).rstd
+    s, r, g = x.double(), rstd.double()[..., None], dy.double() * w.double()
+    mean = (g * s * r).mean(3, keepdim=True)
+    want = r * (g - s * r * mean) + ds.double()
+    # as in the norm's own tests: fp32 errors of 2^-18 against the terms, and the rounding of the result
+    terms = r * (g.abs() + (s * r).abs() * (g * s * r).abs().mean(3, keepdim=True)) + ds.double().abs()
+    dx, _ = norm.backward(dy, x, rstd, w, d_sum=ds)
+    assert bool(((dx.double() - want).abs() <= terms * 2.0 ** -18 + want.abs() * torch.finfo(dtype).eps / 2).all())
