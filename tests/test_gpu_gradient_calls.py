@@ -2,11 +2,14 @@
 head kinds, heads of unlike layouts beside each other."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
-from grad_util import assert_grads, reference
-from parity_util import cuda_err
+import oracle
+import synthetic
+from grad_util import allowed_blocks, assert_grads, reference
+from parity_util import cuda_err, keep_for_head
 
 pytestmark = pytest.mark.gpu
 
@@ -17,7 +20,7 @@ else:
     vsa = _lib = None
 
 BF, F32 = torch.bfloat16, torch.float32
-S_, T_ = 0, 1
+S_, T_, C_ = 0, 1, 2
 
 
 def _rand(*shape, seed=0, dtype=BF):
@@ -375,3 +378,103 @@ def test_norm_gradient_of_tiny_rows(d, dtype):
     terms = r * (g.abs() + (s * r).abs() * (g * s * r).abs().mean(3, keepdim=True)) + ds.double().abs()
     dx, _ = norm.backward(dy, x, rstd, w, d_sum=ds)
     assert bool(((dx.double() - want).abs() <= terms * 2.0 ** -18 + want.abs() * torch.finfo(dtype).eps / 2).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_call_of_heads_of_every_kind(dtype):
+    """Spatial, temporal and cube heads in one call: heads of N and of R rows, blocks past a head's last."""
+    H, F, Hl, Wl, d = 3, 5, 7, 9, 64 if dtype == F32 else 128
+    wl = synthetic.Workload("m", 1, H, F, Hl, Wl, d, 128, "bf16" if dtype == BF else "f32", "given", topk=2)
+    q, k, v = (x.cuda() for x in synthetic.make_qkv(wl))
+    do, d_lse = _rand(*q.shape, seed=9, dtype=dtype), _rand(*q.shape[:3], seed=8, dtype=F32)
+    kinds = torch.tensor([S_, T_, C_], dtype=torch.uint8, device="cuda")
+    plan = vsa.SparseAttention(1, H, F, Hl, Wl, d, 128, dtype=dtype, select="given", w_s=0, w_t=13, topk=2, cube=wl.cube, with_grad=True)
+    o_lo = torch.full_like(q, 7.0)
+    o, lse = plan(q, k, v, kinds=kinds, o_lo=o_lo)
+    grads = plan.backward(do, q, k, v, o, lse, kinds=kinds, d_lse=d_lse)
+    exact = plan.backward(do, q, k, v, o, lse, kinds=kinds, d_lse=d_lse, o_lo=o_lo)
+    assert plan.device_error() == 0
+    for h, kind in enumerate([S_, T_, C_]):
+        q16, k16, v16, do16, o16 = (x[0, h].to(BF) for x in (q, k, v, do, o))
+        al = allowed_blocks(keep_for_head(kind, wl, 0, 13, q16.cpu(), k16.cpu()), oracle.layout_slots(kind, F, Hl, Wl, wl.cube), 128).cuda()
+        assert not al.all()
+        _, _, want, bounds = reference(q16, k16, v16, do16, al, o=o16, lse=lse[0, h], d_lse=d_lse[0, h])
+        assert_grads([g[0, h] for g in grads], want, bounds, f"kind {kind}")
+        _, _, want, bounds = reference(q16, k16, v16, do16, al, d_lse=d_lse[0, h], own_o=True)
+        assert_grads([g[0, h] for g in exact], want, [1.1 * x for x in bounds], f"exact: kind {kind}")
+
+
+@pytest.mark.parametrize("lo", [False, True])
+def test_lists_with_a_set_for_each_layout(lo):
+    """Spatial heads from the natural set, the others from the permuted one, each set with its own O, log-sum-exp, their
+    gradients and O's rounding errors; what a head does not use is NaN and stays as it is."""
+    H, F, Hl, Wl, d, nan = 3, 5, 7, 9, 128, float("nan")
+    wl = synthetic.Workload("m", 1, H, F, Hl, Wl, d, 128, "bf16", "given", topk=2)
+    q, k, v = (x.cuda() for x in synthetic.make_qkv(wl))
+    do, d_lse = _rand(*q.shape, seed=9), _rand(*q.shape[:3], seed=8, dtype=F32)
+    kinds_list = [T_, S_, C_]
+    kinds, err = torch.tensor(kinds_list, dtype=torch.uint8, device="cuda"), cuda_err()
+    shape = _lib.make_shape(1, H, F, Hl, Wl, d, 128, wl.cube)
+    R, nblk = _lib.vsa_layout_rows(shape), _lib.vsa_num_blocks(shape)
+    assert R > wl.N
+    idx, cnt = np.full((1, H, nblk, nblk), -1, np.int32), np.zeros((1, H, nblk), np.int32)
+    o, o_lo, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(1, H, wl.N, device="cuda")
+    masks, slots = [], []
+    for h, kind in enumerate(kinds_list):
+        keep = keep_for_head(kind, wl, 0, 13, q[0, h].cpu(), k[0, h].cpu())
+        i, c = oracle.keep_to_lists(keep, nblk)
+        idx[0, h, :keep.shape[0]], cnt[0, h, :keep.shape[0]] = i, c
+        slots.append(torch.as_tensor(oracle.layout_slots(kind, F, Hl, Wl, wl.cube)).long().cuda())
+        masks.append(allowed_blocks(keep, slots[h].cpu(), 128).cuda())
+        o64, l64, _, _ = reference(q[0, h], k[0, h], v[0, h], do[0, h], masks[h])
+        o[0, h], lse[0, h] = o64.to(BF), l64.float()
+        o_lo[0, h] = (o64 - o[0, h].double()).to(BF)
+    idx, cnt = torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()
+
+    def sets(x):
+        nat, perm = torch.full_like(x, nan), torch.full((1, H, R, *x.shape[3:]), nan, dtype=x.dtype, device="cuda")
+        for h, kind in enumerate(kinds_list):
+            if kind == S_:
+                nat[0, h] = x[0, h]
+            else:
+                perm[0, h] = 0
+                perm[0, h, slots[h]] = x[0, h]
+        return nat, perm
+
+    both = [sets(x) for x in (q, k, v, o, do, lse)]
+    dl, rest = sets(d_lse), sets(o_lo)
+    grads = [(torch.full_like(q, 9.0), torch.full((1, H, R, d), 9.0, dtype=BF, device="cuda")) for _ in range(3)]
+    nat, perm = (_lib.qkvo_grad(*(x[i] for x in both), *(x[i] for x in grads), d_lse=dl[i], o_lo=rest[i] if lo else None) for i in (0, 1))
+    ws = torch.full((_lib.vsa_sparse_attn_bwd_workspace_size(shape),), 0x7f, dtype=torch.uint8, device="cuda")
+    _lib.vsa_sparse_attn_bwd(nat, perm, kinds, idx, cnt, nblk, shape, 0.0, ws, ws.numel(), err)
+    assert _lib.vsa_get_device_error(err) == 0
+    for h, kind in enumerate(kinds_list):
+        used = kind != S_
+        got = [g[used][0, h][slots[h]] if used else g[0][0, h] for g in grads]
+        args = (q[0, h], k[0, h], v[0, h], do[0, h], masks[h])
+        if lo:
+            # o + o_lo is the exact O but for half a step of o_lo, far below P_REL of it
+            _, _, want, bounds = reference(*args, d_lse=d_lse[0, h], own_o=True)
+        else:
+            _, _, want, bounds = reference(*args, o=o[0, h], lse=lse[0, h], d_lse=d_lse[0, h])
+        assert_grads(got, want, [1.1 * x for x in bounds] if lo else bounds, f"kind {kind}")
+        for g in grads:
+            assert (g[not used][0, h] == 9).all()
+            if kind == T_:                       # rows behind the head's last block are not its own
+                assert (g[1][0, h, -(-wl.N // 128) * 128:] == 9).all() and (g[1][0, h, wl.N:-(-wl.N // 128) * 128] == 0).all()
+
+
+def test_codes_of_blocks_with_infinities():
+    """The exponent of the largest float and saturated codes for the infinities; the block's other values by it."""
+    shape = _lib.make_shape(1, 1, 1, 1, 256, 128, 128)
+    x = _rand(1, 1, 256, 128, seed=1)
+    x[0, 0, 3, 5], x[0, 0, 4, 6], x[0, 0, 5, 7] = float("inf"), -float("inf"), 3e38
+    codes, exps = torch.zeros(1, 1, 256, 128, dtype=torch.uint8, device="cuda"), torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    kinds, err = torch.zeros(1, dtype=torch.uint8, device="cuda"), cuda_err()
+    _lib.vsa_quantize_fp8(x, None, kinds, shape, codes, exps, err)
+    assert _lib.vsa_get_device_error(err) == 0 and exps[0, 0] == 120 and exps[0, 1] < 0
+    v = codes.view(torch.float8_e4m3fn).float()
+    # 3e38 = 225.7 * 2^120, and e4m3 steps by 16 there
+    assert v[0, 0, 3, 5] == 448 and v[0, 0, 4, 6] == -448 and v[0, 0, 5, 7] == 224
+    small = x[0, 0, :128].abs() < 1e30
+    assert (v[0, 0, :128][small] == 0).all()      # all far below the smallest code
