@@ -100,6 +100,14 @@ def _no_capture(what: str):
                            f"its backward method instead")
 
 
+def _check_outputs(plan, out, lse):
+    """Outputs that a caller gives are written as whole rows from their first address."""
+    for t, dtype, n, what in ((out, plan.dtype, plan.B * plan.H * plan.N * plan.d, "out"),
+                              (lse, torch.float32, plan.B * plan.H * plan.N, "lse")):
+        if t is not None and (t.dtype != dtype or t.device != plan.device or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {plan.device}")
+
+
 class _Attend(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, q, k, v, kinds):
@@ -204,6 +212,7 @@ class SparseAttention(_HostPipelined):
                 raise ValueError("q, k, v must be contiguous tensors of the configured dtype and device")
             if tuple(t.shape) != (self.B, self.H, self.N, self.d):
                 raise ValueError(f"expected shape {(self.B, self.H, self.N, self.d)}, got {tuple(t.shape)}")
+        _check_outputs(self, out, lse)
         if self.select == VSA_SELECT_GIVEN and kinds is None:
             raise ValueError("select='given' needs kinds")
         with _on(stream, self.device):
@@ -351,6 +360,7 @@ class SemanticAttention(_HostPipelined):
                 raise ValueError("q, k, v must be contiguous bf16 tensors on the configured device")
             if tuple(t.shape) != (self.B, self.H, self.N, self.d):
                 raise ValueError(f"expected shape {(self.B, self.H, self.N, self.d)}, got {tuple(t.shape)}")
+        _check_outputs(self, out, lse)
         with _on(stream, self.device):
             if out is None:
                 out = torch.empty_like(q)

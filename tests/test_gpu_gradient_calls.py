@@ -478,3 +478,25 @@ def test_codes_of_blocks_with_infinities():
     assert v[0, 0, 3, 5] == 448 and v[0, 0, 4, 6] == -448 and v[0, 0, 5, 7] == 224
     small = x[0, 0, :128].abs() < 1e30
     assert (v[0, 0, :128][small] == 0).all()      # all far below the smallest code
+
+
+@pytest.mark.parametrize("which", ["sparse", "semantic"])
+def test_given_outputs_are_checked(which):
+    """An output or a log-sum-exp that is not whole rows of its type would be written over its neighbours."""
+    if which == "sparse":
+        plan, q, k, v, _ = _small()
+        kw = dict(kinds=torch.tensor([S_, T_], dtype=torch.uint8, device="cuda"))
+    else:
+        plan, kw = vsa.SemanticAttention(1, 2, 5, 6, 10, 64, 64, cq=4, ck=4, iters=2, with_lse=True), {}
+        q, k, v = (_rand(1, 2, 300, 64, seed=s) for s in range(3))
+    longer, rows = torch.zeros(1, 2, 301, 64, dtype=BF, device="cuda"), torch.zeros(1, 2, 301, device="cuda")
+    lse = torch.empty(1, 2, 300, device="cuda")
+    for out in (longer[:, :, 1:], q.float(), longer, q.cpu()):
+        with pytest.raises(ValueError, match="out"):
+            plan(q, k, v, out=out, **kw)
+    for bad in (rows[:, :, 1:], lse.double(), rows, lse.cpu()):
+        with pytest.raises(ValueError, match="lse"):
+            plan(q, k, v, lse=bad, **kw)
+    o, _ = plan(q, k, v, **kw)
+    out, l2 = plan(q, k, v, out=torch.empty_like(q), lse=lse, **kw)
+    assert torch.equal(out, o) and l2 is lse
