@@ -234,9 +234,10 @@ class SparseAttention(_HostPipelined):
                  lse: torch.Tensor, kinds: Optional[torch.Tensor] = None, d_lse: Optional[torch.Tensor] = None,
                  out: Optional[Sequence[torch.Tensor]] = None, stream=None, o_lo: Optional[torch.Tensor] = None):
         """Gradients (dq, dk, dv) of a call of this plan, from its inputs, its outputs (``o_lo`` among
-        them, where the call filled it) and the gradients of those (``lse`` and ``d_lse`` with any strides).  ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy,
-        where another call comes between); they are not needed for select="cube".  Nothing else of the
-        call is kept: the masks are built again.  Asynchronous on ``stream``; can be captured."""
+        them, where the call filled it) and the gradients of those (``lse`` and ``d_lse`` with any strides).
+        ``kinds`` are the call's: as given, or ``plan.kinds`` as the call left them (a copy, where another
+        call comes between); they are not needed for select="cube".  Nothing else of the call is kept: the
+        masks are built again.  Asynchronous on ``stream``; can be captured."""
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
         shape = (self.B, self.H, self.N, self.d)
@@ -410,8 +411,8 @@ class RMSNorm:
     of d = 64 or 128), or of whole hidden rows (H = 1): y = s * rstd * weight, s = x + residual.
 
     quantize: 0 for y in the rows' dtype; 1 for e4m3 codes with one power-of-two scale per row; 64 or 128 for
-              one per so many consecutive rows of a head (d = 64 or 128), the codes and exponents
-              ``vsa_sparse_attn_fwd_fp8qk`` takes.  ``keep_y`` writes y as well.
+              one per so many consecutive rows of a head (d = 64 or 128): with 128, the codes and exponents
+              ``vsa_sparse_attn_fwd_fp8qk`` takes for spatial heads.  ``keep_y`` writes y as well.
     with_grad: the plan also holds the workspace of the weight's gradient (``backward``, ``normalise``); that
               workspace serves one call at a time.
 
@@ -484,8 +485,9 @@ class RMSNorm:
     def backward(self, dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
                  d_sum: Optional[torch.Tensor] = None, stream=None, dsum: Optional[torch.Tensor] = None):
         """(dx, d_weight) of a call: s is its x, or its sum where it had a residual; dy and d_sum (or dsum, another
-        name of it) the gradients of y and of sum.  dx is the residual's gradient too, and has s's order of dimensions where s fills its
-        memory (else it is contiguous); d_weight is fp32 (None without a weight).  Asynchronous on ``stream``; can be captured."""
+        name of it) the gradients of y and of sum.  dx is the residual's gradient too, and has s's order of
+        dimensions where s fills its memory (else it is contiguous); d_weight is fp32 (None without a weight).
+        Asynchronous on ``stream``; can be captured."""
         if not self.with_grad:
             raise ValueError("the plan was made without with_grad=True")
         if dsum is not None:

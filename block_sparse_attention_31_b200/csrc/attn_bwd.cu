@@ -24,12 +24,15 @@
 // Why the mean key.  The sum of dS over a row is known (d_lse; 0 without one), and what all of a row's keys
 // have in common drops out of dQ.  It does not drop out of errors: rounding dS to bf16, and a delta that is
 // off, leave a sum e that adds e m to dQ.  The query CTA adds up e in fp32 and takes e m off again.  Without
-// it dQ measured 0.0043 (2-norm, relative) from 64 bits on keys with a common part twice their own size,
-// against 0.0024 with it; the eighth product costs 0.4 of 3.7 ms (12 heads x 32760 rows, d 128, 21% kept).
-// A block's unweighted mean key instead, one K = 16 step, was faster by 0.1 ms but left 0.0036 to 0.0041.
+// it dQ measured 0.0043 (2-norm, relative) from the gradient of the given O in 64 bits on keys with a common part
+// twice their own size, against 0.0024 with it; the eighth product costs 0.4 of 3.7 ms (12 heads x 32760 rows, d 128,
+// 21% kept).  A block's unweighted mean key instead, one K = 16 step, was faster by 0.1 ms but left 0.0036 to 0.0041.
+// With a bf16 O alone the sum of a row is not known so well, and dQ was 0.0093 from the gradient of the unrounded
+// attention; with O's rounding errors beside it 0.0025.  dK takes delta as it is, in which the forward call's rounding
+// of P is left: 0.0025 to 0.0027.  Rounding P, dS and the result to bf16 alone comes to 0.0024.
 //
-// What bounds it.  Executed products run at 1500 TFLOP/s there (0.91 of cuBLAS's burst; back to back the power cap
-// holds both to the same 0.9 of the sustained rate).  A key block's loop takes 2500 cycles for 2048 of
+// What bounds it.  3.66 ms there after a pause: executed products at 1480 TFLOP/s (0.89 of cuBLAS's burst); back to
+// back 4.04 ms under the power cap, 1340 (0.96 of the sustained rate).  A key block's loop takes 2500 cycles for 2048 of
 // tensor time: the threads' chain S -> exponentials (MUFU, 1024) -> dP -> dS is the longer one.  What made it so short:
 // S is freed as soon as it has been read, so that the next block's S runs under the exponentials; P and dS go over
 // dP; barriers are tested ahead; the issuing lane is elected, which lets tcgen05.mma run ahead of it (8 products

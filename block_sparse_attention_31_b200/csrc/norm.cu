@@ -11,10 +11,10 @@
 // thread has several loads in flight.  At 6.5 TB/s an SM has some 12 instructions for an element, so the
 // arithmetic runs on packed pairs (f32x2) and a thread holds at least 16 elements of a row where it can:
 // what a row costs once (its reduction, root and exponent) is shared by them.  Measured, of the 6.54 TB/s copy:
-// 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 35 us (0.89), to codes per 128 rows 33.5 us (0.69; 43 with
-// a CTA a block, whose maximum stands between its loads and its stores), 32760 rows of 1536 with residual, sum and
-// codes 58.5 us (0.92); gradients of the first 54.5 us (0.85) and of rows of 1536 81.5 us (0.75), 56.5 and 84 without
-// the next chunk's loads under the work on one.  All arithmetic is fp32; y, sum and dx are rounded once, when they
+// with L2 flushed before each: 12 heads x 32760 rows of 128 bf16 read from [B, N, H, d] 36 us (0.86), to codes per 128
+// rows 34.5 us (0.67; 43 with a CTA a block, whose maximum stands between its loads and its stores), 32760 rows of 1536
+// with residual, sum and codes 59 us (0.91); gradients of the first 58 us (0.80) and of rows of 1536 84 us (0.73), 2 to
+// 2.5 us more without the next chunk's loads under the work on one.  All arithmetic is fp32; y, sum and dx are rounded once, when they
 // are written, and y is normalised from the sum before its rounding.
 #include <cfloat>
 

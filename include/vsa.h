@@ -318,7 +318,8 @@ VSA_API vsa_status vsa_sparse_attn_fwd_natural(const vsa_qkvo *natural, const ui
  *   natural   [B, H, N, d] bf16 (or [B, H, R, d] when permuted is NULL);  permuted [B, H, R, d]
  *   dst       [B, H, R, d] e4m3 codes (caller-owned device memory); rows past a head's own
  *             rows are zero
- *   d_exp     [B*H, nblk] int32 out: the exponent e of every block's scale
+ *   d_exp     [B*H, nblk] int32 out: the exponent e of every block's scale; 120 for a block with
+ *             an infinity, whose code is that of 448
  * d must be 128 (VSA_ERR_UNSUPPORTED otherwise); a bad kind byte sets VSA_DEVERR_KIND.
  */
 VSA_API vsa_status vsa_quantize_fp8(const void *natural, const void *permuted, const uint8_t *d_kind,
@@ -398,7 +399,8 @@ typedef struct {
     const float *d_lse;           /* gradient of lse, or NULL */
     void *dq, *dk, *dv;
     const void *o_lo;             /* what rounding o to bf16 left over (vsa_attention_train), or NULL;
-                                     given in every set that is read, or it counts for nothing */
+                                     given in every set that is read, or it counts for nothing.  Only
+                                     where the lists hold every key that lse counts: see below */
 } vsa_qkvo_grad;
 
 /* Workspace bytes of vsa_sparse_attn_bwd: a bitset of the lists (B*H*nblk*ceil(nblk/32) words)
@@ -412,11 +414,12 @@ VSA_API size_t vsa_sparse_attn_bwd_workspace_size(const vsa_shape *shape);
  * P and dS are rounded to bf16 in front of their tensor products, every sum is fp32, the
  * gradients are bf16.  Each is written by one owner: two runs give the same bits.  What rounding dS adds to
  * its sum over a row is taken off dq again.  delta takes o as it is given: the error of a bf16 o moves a
- * row's dq by that error times the row's mean key.  With o_lo delta is exact, and the sum of dS over a
- * row is held to what it then is, d_lse (a sixth more time).
- *   natural, permuted   as for vsa_sparse_attn_fwd (permuted may be NULL); bf16; padding slots
- *                       of cube layouts hold finite values, zero as vsa_permute leaves them.
- *                       Every row of a head's layout is written, rows that hold no token or
+ * row's dq by that error times the row's mean key.  With o_lo the sum of dS over a row is held to what it
+ * then is, d_lse.  That is its sum over all keys of the row: a caller who splits a row's keys over several
+ * calls under one lse leaves o_lo out of them.
+ *   natural, permuted   as for vsa_sparse_attn_fwd (permuted may be NULL); bf16; slots that hold
+ *                       no token (cube padding, the rest of a last block) hold finite values,
+ *                       zero as vsa_permute leaves them.  Every row of a head's layout is written, rows that hold no token or
  *                       that nothing sees with zeros
  *   d_kind, d_kv_idx, d_kv_cnt, max_kv, scale   the forward call's.  A malformed list sets
  *                       VSA_DEVERR_KV_RANGE and counts as empty, as in the forward call; a bad
@@ -451,7 +454,8 @@ VSA_API size_t vsa_attention_bwd_workspace_size(const vsa_shape *shape, const vs
  * Gradient of vsa_attention: permute -> masks -> vsa_sparse_attn_bwd -> unpermute, on `stream`.
  * The masks are built again from the kinds (and, for cube heads, from q and k), so nothing of
  * the forward call's workspace is needed.
- *   io       natural q, k, v, o, d_o, lse (d_lse, o_lo or NULL); dq, dk, dv written; rows in dtype
+ *   io       natural q, k, v, o, d_o, lse (d_lse, o_lo or NULL); dq, dk, dv written; rows in dtype;
+ *            a head of unknown kind sets VSA_DEVERR_KIND and gets zeros
  *   d_kind   [B*H] the kinds the forward call used (given, or as it wrote them)
  *   params   the forward call's; layout_in_kernel is accepted and changes nothing here, qk_fp8
  *            returns VSA_ERR_UNSUPPORTED (the e4m3 codes have no gradient)
@@ -478,8 +482,8 @@ typedef struct {
 } vsa_norm_shape;
 
 /*
- * s = x + residual, rstd = 1 / sqrt(mean(s^2) + eps), y = s * rstd * weight, in fp32; y is taken from
- * s before s is rounded.
+ * s = x + residual, rstd = 1 / sqrt(mean(s^2) + eps), y = s * rstd * weight, in fp32 (a row whose
+ * squares add up to more than a float holds has rstd = 0); y is taken from s before s is rounded.
  *   x, residual  rows in dtype (VSA_F32 or VSA_BF16), strided; residual may be NULL (s = x).  Rows whose
  *                pointers and strides are multiples of 16 bytes are read 16 bytes at a time, others
  *                element by element
@@ -487,8 +491,10 @@ typedef struct {
  *   sum          [B, H, N, d] dtype out: s, or NULL (needs a residual)
  *   y            [B, H, N, d] dtype out, or NULL
  *   codes        [B, H, N, d] e4m3 codes of y / 2^e out, or NULL: nearest even, with one exponent e per
- *                `block` rows, the smallest with max |y| <= 448 * 2^e (0 for all-zero rows), in the
- *                layout vsa_sparse_attn_fwd_fp8qk takes.  y is not rounded to dtype in between.
+ *                `block` rows, the smallest with max |y| <= 448 * 2^e (0 for all-zero rows).  Blocks
+ *                are of rows as they stand, so that vsa_sparse_attn_fwd_fp8qk takes them for spatial
+ *                heads; temporal and cube heads are quantised in their own layout, by
+ *                vsa_quantize_fp8.  y is not rounded to dtype in between.
  *                A NaN has the NaN code; an infinity is saturated, with e = 120
  *   d_exp        [B*H, ceil(N / block)] int32 out (with codes)
  *   rstd         [B, H, N] fp32 out, or NULL
