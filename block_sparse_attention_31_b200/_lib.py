@@ -470,9 +470,10 @@ def vsa_sparse_attn_bwd(natural: QKVOGrad, permuted, kinds, kv_idx, kv_cnt, max_
         _expect(kv_idx, _I32, lists * int(max_kv), "kv_idx")
         _expect(kv_cnt, _I32, lists, "kv_cnt")
         _expect_scratch(ws, ws_bytes, err)
-    natural, copies = _whole_rows(natural, stream)
-    permuted, more = _whole_rows(permuted, stream)
-    _check(lib.vsa_sparse_attn_bwd(ctypes.byref(natural), ctypes.byref(permuted) if permuted is not None else None,
+    # (the caller's sets, and the copies, hold their tensors until the launch)
+    nat, copies = _whole_rows(natural, stream)
+    perm, more = _whole_rows(permuted, stream)
+    _check(lib.vsa_sparse_attn_bwd(ctypes.byref(nat), ctypes.byref(perm) if perm is not None else None,
                                    _ptr(kinds), _ptr(kv_idx), _ptr(kv_cnt), int(max_kv), ctypes.byref(shape),
                                    float(scale), _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)),
            "vsa_sparse_attn_bwd")
@@ -488,8 +489,8 @@ def vsa_attention_bwd(io: QKVOGrad, dtype: int, shape: Shape, params: Params, ki
         _expect_set(io, geometry[0] * geometry[1], shape.d, dtypes, "call's")
         _expect(kinds, _U8, geometry[0], "kinds")
         _expect_scratch(ws, ws_bytes, err)
-    io, copies = _whole_rows(io, stream)
-    _check(lib.vsa_attention_bwd(ctypes.byref(io), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
+    whole, copies = _whole_rows(io, stream)
+    _check(lib.vsa_attention_bwd(ctypes.byref(whole), dtype, ctypes.byref(shape), ctypes.byref(params), _ptr(kinds),
                                  _ptr(ws), int(ws_bytes), _ptr(err), _stream(stream)), "vsa_attention_bwd")
 
 

@@ -1,6 +1,7 @@
 """CPU checks of what the binding makes of the gradient's arguments.  No kernel runs: the library's entry point is
 replaced by one that reads its arguments back."""
 import ctypes
+import weakref
 
 import pytest
 import torch
@@ -197,3 +198,19 @@ def test_norm_refuses_what_would_be_read_as_something_else(monkeypatch):
             bwd(dx=short, s=proj, sh=views)
     with pytest.raises(ValueError, match="workspace"):
         bwd(wsb=101)
+
+
+def test_tensors_of_a_set_live_until_the_launch(monkeypatch):
+    """A set that nothing else holds, with a log-sum-exp that has to be copied."""
+    shape, refs, alive = _lib.make_shape(1, 2, 4, 8, 8, 64, 64), [], []
+    monkeypatch.setattr(_lib.lib, "vsa_sparse_attn_bwd", lambda *a: alive.extend(r() is not None for r in refs) or _lib.VSA_OK)
+
+    def fresh():
+        t = {**_set(), "lse": torch.zeros(2, 257)[:, :256]}
+        refs.extend(weakref.ref(x) for x in t.values())
+        return _lib.qkvo_grad(**t)
+
+    ws = torch.zeros(_lib.vsa_sparse_attn_bwd_workspace_size(shape), dtype=torch.uint8)
+    _lib.vsa_sparse_attn_bwd(fresh(), fresh(), torch.zeros(2, dtype=torch.uint8), torch.zeros(1, 2, 4, 1, dtype=torch.int32),
+                             torch.ones(1, 2, 4, dtype=torch.int32), 1, shape, 0.0, ws, ws.numel(), torch.zeros(1, dtype=torch.int32), 0)
+    assert len(alive) == 18 and all(alive)
