@@ -1,6 +1,6 @@
 """ctypes binding of libvsa.so: one Python function per C entry point, same names.
 
-Argument marshalling only -- every step of the attention path runs in the library's CUDA
+Argument marshalling and its checks only -- every step of the attention path runs in the library's CUDA
 kernels.  PyTorch provides device memory and streams.  There is no CPU fallback: if the
 library cannot be loaded, importing this module raises.
 """
